@@ -3,6 +3,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -10,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfckl.so")
 SOURCES = ["fckl.cu"]
-HEADERS = ["ptx.cuh", "gemm.cuh", "epilogues.cuh", "rows.cuh"]
+HEADERS = ["ptx.cuh", "reduce.cuh", "gemm.cuh", "epilogues.cuh", "rows.cuh", "host.cuh"]
 
 
 def nvcc_path() -> str:
@@ -28,20 +30,33 @@ def needs_rebuild() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and not needs_rebuild():
-        return LIB
-    cmd = [nvcc_path(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a",
-           "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-shared", "-I", INCLUDE, "-I", CSRC,
-           "-o", LIB + ".tmp"] + list(extra) + [os.path.join(CSRC, f) for f in SOURCES]
+def _run(cmd, verbose) -> bool:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libfckl.so")
-    if verbose and (r.stdout or r.stderr):
+    elif verbose and (r.stdout or r.stderr):
         print(r.stdout + r.stderr)
+    return r.returncode == 0
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    if not force and not needs_rebuild():
+        return LIB
+    flags = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
+             "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC] + list(extra)
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, f + ".o") for f in SOURCES]
+        cmds = [[nvcc_path()] + flags + ["-c", os.path.join(CSRC, f), "-o", o]
+                for f, o in zip(SOURCES, objs)]
+        with ThreadPoolExecutor() as pool:  # one nvcc per translation unit
+            done = list(pool.map(lambda c: _run(c, verbose), cmds))
+        if all(done):
+            done.append(_run([nvcc_path(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a",
+                              "-o", LIB + ".tmp"] + objs, verbose))
+    if not all(done):
+        raise RuntimeError("nvcc failed building libfckl.so")
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

@@ -7,27 +7,12 @@
 #include <cuda_bf16.h>
 
 #include "gemm.cuh"
+#include "reduce.cuh"
 
 namespace fckl {
 
 constexpr int ROW_WARPS = 8;  // rows per 256-thread block in the warp-per-row kernels
 constexpr int K_MAX = 256;
-
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-__device__ __forceinline__ int warp_sum_int(int x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
 
 // N_valid = #rows with row_mask != 0 (N when there is no mask), or the
 // caller's total (> 0) when the rows are one shard of a larger batch.  One block.
@@ -135,33 +120,6 @@ __global__ void __launch_bounds__(128)
 __device__ __forceinline__ uint32_t float_key(float f) {
   const uint32_t b = __float_as_uint(f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-// Exclusive block-wide prefix sum of one int per thread (blockDim.x = 1024).
-__device__ __forceinline__ int block_exclusive_scan(int v, int* sh, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int w = lane < (int)(blockDim.x >> 5) ? sh[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    sh[lane] = w;  // inclusive warp totals
-  }
-  __syncthreads();
-  const int before = (warp > 0 ? sh[warp - 1] : 0) + x - v;
-  *total = sh[(blockDim.x >> 5) - 1];
-  __syncthreads();
-  return before;
 }
 
 // Row indices of the valid rows (row_mask != 0), ascending, into list[0, n),
