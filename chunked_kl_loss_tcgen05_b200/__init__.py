@@ -22,6 +22,9 @@ __all__ = [
     "fckl_status_string", "FcklKernelStat", "fckl_profile_begin", "fckl_profile_end",
     "fckl_fwd_noalloc", "fckl_student_entropy", "fckl_select_top_rows", "fckl_fwd_bwd_rows",
     "fckl_host_workspace_bytes", "fckl_fwd_bwd_host", "fckl_fwd_bwd_sliced",
+    "FcklCeProblem", "FCKL_REDUCE_MEAN", "FCKL_REDUCE_SUM", "FCKL_LABELS_INT", "FCKL_LABELS_LONG",
+    "FCKL_GRAD_FLOAT", "FCKL_GRAD_BFLOAT", "fckl_ce_workspace_bytes", "fckl_ce_fwd",
+    "fckl_ce_fwd_bwd", "fckl_ce_bwd", "fckl_scale_gradient",
 ]
 
 FCKL_OK = 0
@@ -41,11 +44,15 @@ exported_symbols = ("fckl_workspace_bytes", "fckl_resolved_chunk", "fckl_fwd", "
                     "fckl_check", "fckl_status_string", "fckl_profile_begin", "fckl_profile_end",
                     "fckl_fwd_noalloc", "fckl_student_entropy", "fckl_select_top_rows",
                     "fckl_fwd_bwd_rows", "fckl_host_workspace_bytes", "fckl_fwd_bwd_host",
-                    "fckl_fwd_bwd_sliced")
+                    "fckl_fwd_bwd_sliced", "fckl_ce_workspace_bytes", "fckl_ce_fwd",
+                    "fckl_ce_fwd_bwd", "fckl_ce_bwd", "fckl_scale_gradient")
 
 
 FCKL_TEACHER_LOGITS = 0
 FCKL_TEACHER_PROBS = 1
+FCKL_REDUCE_MEAN, FCKL_REDUCE_SUM = 0, 1
+FCKL_LABELS_INT, FCKL_LABELS_LONG = 0, 1
+FCKL_GRAD_FLOAT, FCKL_GRAD_BFLOAT = 0, 1
 
 
 class FcklProblem(ctypes.Structure):
@@ -59,6 +66,23 @@ class FcklProblem(ctypes.Structure):
                  dw_rows=0):
         super().__init__(int(N), int(H), int(V), int(K), float(T), int(chunk), int(teacher),
                          int(n_valid_total), int(dw_rows))
+
+
+class FcklCeProblem(ctypes.Structure):
+    """Mirror of ``fckl_ce_problem``."""
+    _fields_ = [("N", ctypes.c_int64), ("H", ctypes.c_int64), ("V", ctypes.c_int64),
+                ("T", ctypes.c_float), ("label_smoothing", ctypes.c_float),
+                ("z_loss", ctypes.c_float), ("reduction", ctypes.c_int32),
+                ("ignore_index", ctypes.c_int64), ("chunk", ctypes.c_int64),
+                ("n_valid_total", ctypes.c_int64), ("label_type", ctypes.c_int32),
+                ("grad_type", ctypes.c_int32)]
+
+    def __init__(self, N, H, V, T=1.0, label_smoothing=0.0, z_loss=0.0,
+                 reduction=FCKL_REDUCE_MEAN, ignore_index=-100, chunk=0, n_valid_total=0,
+                 label_type=FCKL_LABELS_LONG, grad_type=FCKL_GRAD_FLOAT):
+        super().__init__(int(N), int(H), int(V), float(T), float(label_smoothing), float(z_loss),
+                         int(reduction), int(ignore_index), int(chunk), int(n_valid_total),
+                         int(label_type), int(grad_type))
 
 
 class FcklKernelStat(ctypes.Structure):
@@ -119,6 +143,17 @@ def load() -> ctypes.CDLL:
     lib.fckl_fwd_bwd_rows.restype = ctypes.c_int
     lib.fckl_fwd_noalloc.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.fckl_fwd_noalloc.restype = ctypes.c_int
+    Q, i32 = ctypes.POINTER(FcklCeProblem), ctypes.c_int32
+    lib.fckl_ce_workspace_bytes.argtypes = [Q, i32]
+    lib.fckl_ce_workspace_bytes.restype = sz
+    lib.fckl_ce_fwd.argtypes = [Q] + [vp] * 7 + [vp, sz, vp]
+    lib.fckl_ce_fwd.restype = ctypes.c_int
+    lib.fckl_ce_fwd_bwd.argtypes = [Q] + [vp] * 9 + [vp, sz, vp]
+    lib.fckl_ce_fwd_bwd.restype = ctypes.c_int
+    lib.fckl_ce_bwd.argtypes = [Q] + [vp] * 7 + [vp, sz, vp]
+    lib.fckl_ce_bwd.restype = ctypes.c_int
+    lib.fckl_scale_gradient.argtypes = [vp, ctypes.c_int64, i32, vp, vp]
+    lib.fckl_scale_gradient.restype = ctypes.c_int
     lib.fckl_profile_begin.argtypes = [ctypes.c_uint32]
     lib.fckl_profile_begin.restype = None
     lib.fckl_profile_end.argtypes = [ctypes.POINTER(FcklKernelStat), ctypes.c_int]
@@ -219,6 +254,36 @@ def fckl_fwd_bwd_rows(prob, hidden, W, topk_idx, topk_logit, rows, n_rows, loss,
                                         _ptr(stream)))
 
 
+def fckl_ce_workspace_bytes(prob: FcklCeProblem, gradients) -> int:
+    return int(load().fckl_ce_workspace_bytes(ctypes.byref(prob), 1 if gradients else 0))
+
+
+def fckl_ce_fwd(prob, hidden, W, labels, row_weight, loss, row_loss, lse, workspace,
+                workspace_bytes, stream) -> int:
+    """Array arguments are device addresses (ints) or None; returns the status."""
+    return load().fckl_ce_fwd(ctypes.byref(prob), hidden, W, labels, row_weight, loss, row_loss,
+                              lse, workspace, workspace_bytes, stream)
+
+
+def fckl_ce_fwd_bwd(prob, hidden, W, labels, row_weight, loss, row_loss, lse, dH, dW, workspace,
+                    workspace_bytes, stream) -> int:
+    """Array arguments are device addresses (ints) or None; returns the status."""
+    return load().fckl_ce_fwd_bwd(ctypes.byref(prob), hidden, W, labels, row_weight, loss,
+                                  row_loss, lse, dH, dW, workspace, workspace_bytes, stream)
+
+
+def fckl_ce_bwd(prob, hidden, W, labels, lse, row_grad, dH, dW, workspace, workspace_bytes,
+                stream) -> int:
+    """Array arguments are device addresses (ints) or None; returns the status."""
+    return load().fckl_ce_bwd(ctypes.byref(prob), hidden, W, labels, lse, row_grad, dH, dW,
+                              workspace, workspace_bytes, stream)
+
+
+def fckl_scale_gradient(grad, n, grad_type, factor, stream) -> int:
+    """Array arguments are device addresses (ints); returns the status."""
+    return load().fckl_scale_gradient(grad, n, grad_type, factor, stream)
+
+
 def fckl_check(workspace, stream) -> int:
     return int(load().fckl_check(_ptr(workspace), _ptr(stream)))
 
@@ -229,7 +294,8 @@ def fckl_status_string(status: int) -> str:
 
 KERNEL_KINDS = ("count_valid", "prep_teacher", "fwd_logits_lse", "merge_loss", "bwd_dlogits",
                 "dH_gemm", "dW_gemm", "finalize", "entropy_gemm", "merge_entropy", "gather_rows",
-                "scatter_rows", "select_rows", "zero_dw")
+                "scatter_rows", "select_rows", "zero_dw", "ce_logits", "ce_dlogits", "dH_rows",
+                "dW_round")
 
 
 def fckl_profile_begin(kinds=None) -> None:
@@ -240,7 +306,7 @@ def fckl_profile_begin(kinds=None) -> None:
     load().fckl_profile_begin(mask)
 
 
-def fckl_profile_end(max_stats: int = 16) -> list:
+def fckl_profile_end(max_stats: int = 32) -> list:
     """Returns a list of dicts (name, launches, total_ms, flops, bytes)."""
     arr = (FcklKernelStat * max_stats)()
     n = int(load().fckl_profile_end(arr, max_stats))

@@ -1,0 +1,397 @@
+// Host side of the vocabulary cross entropy: checks, workspace layout and the
+// chunk loop.  Per chunk of C kept rows, on the caller's stream:
+//   gather rows -> logits GEMM (log-sum-exp epilogue) -> merge (row losses)
+//   [-> recompute GEMM (dlogits epilogue) -> dH GEMM -> dW GEMM -> dH rows].
+#include <algorithm>
+#include <cmath>
+
+#include "ce.cuh"
+#include "fckl.h"
+#include "host.cuh"
+
+using namespace fckl;
+
+namespace {
+
+// Room for the k segments of a chunk's dH GEMM: four units for every CTA pair
+// of a B200 (more would mean more slabs to sum than waves to balance), 256 KB
+// each, or one segment of every tile.
+constexpr int kSlabUnits = 4 * 74;
+
+enum class CeMode { kFwd, kFwdBwd, kBwd };
+
+struct CeLayout {
+  long long C, Vp, NT, NTh, nchunks;
+  int slab_units;
+  size_t off_list, off_share, off_lab, off_kw, off_zlab, off_lse2, off_part, off_zsum, off_h,
+      off_dlog, off_slab, off_dw, total;
+};
+
+bool valid_ce(const fckl_ce_problem* p) {
+  if (p == nullptr) return false;
+  if (p->N < 1 || p->H < 1 || p->V < 1 || p->chunk < 0) return false;
+  if (p->N > INT32_MAX || p->H > INT32_MAX || p->V > INT32_MAX) return false;
+  if (!(std::isfinite(p->T) && p->T > 0.f)) return false;
+  if (!(p->label_smoothing >= 0.f && p->label_smoothing <= 1.f)) return false;
+  if (!(p->z_loss >= 0.f && std::isfinite(p->z_loss))) return false;
+  if (p->label_type != FCKL_LABELS_INT && p->label_type != FCKL_LABELS_LONG) return false;
+  if (p->reduction != FCKL_REDUCE_MEAN && p->reduction != FCKL_REDUCE_SUM) return false;
+  if (p->grad_type != FCKL_GRAD_FLOAT && p->grad_type != FCKL_GRAD_BFLOAT) return false;
+  if (p->n_valid_total < 0 || p->n_valid_total > INT32_MAX) return false;
+  return true;
+}
+
+bool supported_ce(const fckl_ce_problem* p) { return p->H % 8 == 0; }
+
+CeLayout ce_layout(const fckl_ce_problem* p, bool grads) {
+  CeLayout L{};
+  L.C = resolve_rows(p->N, p->V, p->chunk);
+  L.Vp = (long long)align_up((size_t)p->V, 64);
+  L.NT = cdiv(p->V, BN);
+  L.NTh = cdiv(p->H, BN);
+  L.nchunks = cdiv(p->N, L.C);
+  const long long tiles = cdiv(L.C, PM) * L.NTh;
+  L.slab_units = (int)std::min<long long>(std::max<long long>(tiles, kSlabUnits), INT32_MAX);
+  size_t off = align_up(sizeof(DeviceCtl), kAlign);
+  auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, kAlign); return o; };
+  const size_t C = (size_t)L.C;
+  L.off_list = take((size_t)p->N * 4);
+  L.off_share = take((size_t)p->N * 4);
+  L.off_lab = take(C * 4);
+  L.off_kw = take(C * 4);
+  L.off_zlab = take(C * 4);
+  L.off_lse2 = take(C * 4);
+  L.off_part = take(C * L.NT * sizeof(float2));
+  L.off_zsum = take(p->label_smoothing > 0.f ? C * L.NT * 4 : 0);
+  L.off_h = take(C * p->H * 2);
+  L.off_dlog = take(grads ? C * L.Vp * 2 : 0);
+  // S segments of MT row tiles fit when S * MT * NTh <= slab_units
+  L.off_slab = take(grads ? (size_t)(L.slab_units / L.NTh) * PM * p->H * 4 : 0);
+  // bf16 gradients of several chunks are summed in fp32 first
+  L.off_dw = take(grads && L.nchunks > 1 && p->grad_type == FCKL_GRAD_BFLOAT
+                      ? (size_t)p->V * p->H * 4 : 0);
+  L.total = off;
+  return L;
+}
+
+struct CeRequest {
+  CeMode mode = CeMode::kFwd;
+  const fckl_ce_problem* prob = nullptr;
+  const void* hidden = nullptr;
+  const void* W = nullptr;
+  const void* labels = nullptr;
+  const float* factor = nullptr;  // row weight, or the upstream row gradient
+  const float* lse_in = nullptr;
+  float* loss = nullptr;
+  float* row_loss = nullptr;
+  float* lse_out = nullptr;
+  void* dH = nullptr;
+  void* dW = nullptr;
+  void* workspace = nullptr;
+  size_t ws_bytes = 0;
+  void* stream = nullptr;
+};
+
+template <class Epi, bool A_MN, bool B_MN>
+bool allow_smem() {
+  return cudaFuncSetAttribute(gemm_pair_kernel<Epi, A_MN, B_MN>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)pair_smem_bytes<Epi>()) == cudaSuccess;
+}
+
+struct CeDevice {
+  bool ready = false, ok = false;
+  int sms = 0;
+};
+CeDevice g_ce_dev[kMaxDevices];
+std::mutex g_ce_mu;
+
+const CeDevice* ce_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  std::lock_guard<std::mutex> lk(g_ce_mu);
+  CeDevice& d = g_ce_dev[dev];
+  if (!d.ready) {
+    d.ready = true;
+    int major = 0, minor = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    d.ok = major == 10 && minor == 0 && d.sms > 1 && allow_smem<EpiCe<false>, false, false>() &&
+           allow_smem<EpiCe<true>, false, false>() && allow_smem<EpiCeDlogits, false, false>() &&
+           allow_smem<EpiCeDH, false, true>() && allow_smem<EpiCeDW, true, true>() &&
+           allow_smem<EpiCeDWSum, true, true>();
+  }
+  return &d;
+}
+
+template <class Label>
+fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* dev) {
+  const fckl_ce_problem* prob = q.prob;
+  const bool grads = q.mode != CeMode::kFwd;
+  const bool losses = q.mode != CeMode::kBwd;
+  const bool bf16_grads = prob->grad_type == FCKL_GRAD_BFLOAT;
+  const int H = (int)prob->H, V = (int)prob->V;
+  const long long N = prob->N;
+  const Label* labels = static_cast<const Label*>(q.labels);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(q.stream);
+  const bool pdl = pdl_enabled();
+  uint8_t* ws = static_cast<uint8_t*>(q.workspace);
+  DeviceCtl* ctl = reinterpret_cast<DeviceCtl*>(ws);
+  auto at = [&](size_t off) { return static_cast<void*>(ws + off); };
+  int32_t* list = static_cast<int32_t*>(at(L.off_list));
+  float* share = static_cast<float*>(at(L.off_share));
+  int* lab = static_cast<int*>(at(L.off_lab));
+  float* kw = static_cast<float*>(at(L.off_kw));
+  float* zlab = static_cast<float*>(at(L.off_zlab));
+  float* lse2 = static_cast<float*>(at(L.off_lse2));
+  float2* part = static_cast<float2*>(at(L.off_part));
+  float* zsum = static_cast<float*>(at(L.off_zsum));
+  __nv_bfloat16* hst = static_cast<__nv_bfloat16*>(at(L.off_h));
+  __nv_bfloat16* dlog = static_cast<__nv_bfloat16*>(at(L.off_dlog));
+  float* slab = static_cast<float*>(at(L.off_slab));
+  const float invT = 1.f / prob->T, scale2 = kLog2e / prob->T;
+  const CtlArgs ca{ctl, wait_timeout_ns(), 0};
+  const int pairs = dev->sms / 2;
+  const int NT = (int)L.NT, NTh = (int)L.NTh;
+  const int KBh = (int)cdiv(H, BK), KBv = (int)cdiv(V, BK);
+  const int narrow_h = (H % BN != 0 && H % BN <= 128) ? 1 : 0;
+  const bool smooth = prob->label_smoothing > 0.f;
+
+  // Rows by label.  One block takes up to 8192 rows (8 passes of 4096 would
+  // cost more than the second launch and the memset it saves).
+  {
+    const int denom = q.mode == CeMode::kBwd || prob->reduction == FCKL_REDUCE_SUM
+                          ? 1 : (int)prob->n_valid_total;
+    const long long R =
+        N <= 8192 ? 8192
+                  : std::max<long long>(4096, cdiv(cdiv(N, kCompactBlocks), 4096) * 4096);
+    const int nb = (int)cdiv(N, R);
+    ProfScope ps(K_COUNT, st, 0.0, (double)N * (sizeof(Label) * (nb > 1 ? 2 : 1) + 4));
+    if (nb > 1) {
+      if (cudaMemsetAsync(ctl, 0, sizeof(DeviceCtl), st) != cudaSuccess) return FCKL_ERR_CUDA;
+      FCKL_LAUNCH(k_ce_count<Label>, nb, 1024, 0, labels, N, R, (long long)prob->ignore_index, V,
+                  ctl);
+    }
+    FCKL_LAUNCH(k_ce_list<Label>, nb, 1024, 0, labels, N, R, (long long)prob->ignore_index, V,
+                denom, list, ctl);
+  }
+
+  CUtensorMap mapW_k, mapW_mn, mapdW, mapSlab;
+  int w3d = 0;
+  if (!make_map(&mapW_k, q.W, H, V, (long long)H * 2, BK, BN / 2)) return FCKL_ERR_CUDA;
+  // dW goes to the caller (fp32 always; bf16 when one chunk computes all of
+  // it) or to the fp32 sum in the workspace.
+  void* dw_dst = bf16_grads && L.nchunks > 1 ? at(L.off_dw) : q.dW;
+  const bool dw_direct16 = bf16_grads && L.nchunks == 1;
+  if (q.dW) {
+    if (dw_direct16 ? !make_map(&mapdW, dw_dst, H, V, (long long)H * 2, 64, 32)
+                    : !make_map(&mapdW, dw_dst, H, V, (long long)H * 4, 32, 32, true))
+      return FCKL_ERR_CUDA;
+  }
+  if (q.dH) {
+    if (!make_map_mn(&mapW_mn, q.W, H, V, (long long)H * 2, &w3d)) return FCKL_ERR_CUDA;
+    if (!make_map(&mapSlab, slab, H, (long long)(L.slab_units / NTh) * PM, (long long)H * 4, 32, 32,
+                  true))
+      return FCKL_ERR_CUDA;
+  }
+  auto grid_for = [&](long long units) {
+    return (int)(2 * std::max<long long>(1, std::min<long long>(pairs, units)));
+  };
+
+  for (long long c = 0; c < L.nchunks; ++c) {
+    const long long row0 = c * L.C;
+    const int cap = (int)std::min(L.C, N - row0);
+    const int32_t* clist = list + row0;
+    const RowCount rc{-1, ctl, (int)row0, cap};
+    const double nr = (double)cap, flops = 2.0 * nr * V * H;
+    const long long MT = cdiv(cap, PM);
+    {
+      ProfScope ps(K_GATHER, st, 0.0, nr * (H * 4.0 + 16.0));
+      FCKL_LAUNCH(k_ce_gather<Label>, cap, 128, 0, clist, rc, H,
+                  static_cast<const __nv_bfloat16*>(q.hidden), labels, q.factor, q.lse_in, hst, lab,
+                  kw, lse2);
+    }
+    CUtensorMap mapH_k;
+    if (!make_map(&mapH_k, hst, H, cap, (long long)H * 2, BK, CM)) return FCKL_ERR_CUDA;
+    SchedArgs sa_v{SCHED_VOCAB_MAJOR, NT, KBh, 1, 0, rc, 0, 0};
+    const int Gv = grid_for(MT * NT);
+    if (losses) {
+      {
+        ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + nr * NT * 8.0);
+        if (smooth) {
+          EpiCe<true>::Params pf{V, NT, scale2, lab, zlab, part, zsum};
+          FCKL_LAUNCH((gemm_pair_kernel<EpiCe<true>, false, false>), Gv, GEMM_THREADS,
+                      pair_smem_bytes<EpiCe<true>>(), mapH_k, mapW_k, mapW_k, pf, sa_v, ca);
+        } else {
+          EpiCe<false>::Params pf{V, NT, scale2, lab, zlab, part, nullptr};
+          FCKL_LAUNCH((gemm_pair_kernel<EpiCe<false>, false, false>), Gv, GEMM_THREADS,
+                      pair_smem_bytes<EpiCe<false>>(), mapH_k, mapW_k, mapW_k, pf, sa_v, ca);
+        }
+      }
+      ProfScope ps(K_MERGE, st, 0.0, nr * (NT * 8.0 + 28.0));
+      FCKL_LAUNCH(k_ce_merge, (int)cdiv(cap, kCeWarps), kCeWarps * 32, 0, (const float2*)part,
+                  (const float*)(smooth ? zsum : nullptr), NT, rc, cap, V, invT,
+                  prob->label_smoothing, prob->z_loss, clist, (const float*)zlab, (const float*)kw,
+                  lse2, q.row_loss, q.lse_out, share + row0);
+    }
+    if (!grads) continue;
+
+    // The recompute GEMM's operands (the gathered rows, W) were complete before
+    // the merge launched; without a merge it follows the gather directly.
+    SchedArgs sa_b = sa_v;
+    sa_b.early = losses ? 1 : 0;
+    CUtensorMap mapD_st, mapD_k, mapD_mn, mapH_mn;
+    if (!make_map(&mapD_st, dlog, L.Vp, cap, L.Vp * 2, 64, 32)) return FCKL_ERR_CUDA;
+    {
+      EpiCeDlogits::Params pb{V, scale2, prob->label_smoothing, 2.f * prob->z_loss, lab, kw, lse2,
+                              cap};
+      ProfScope ps(K_CE_DLOGITS, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
+      FCKL_LAUNCH((gemm_pair_kernel<EpiCeDlogits, false, false>), Gv, GEMM_THREADS,
+                  pair_smem_bytes<EpiCeDlogits>(), mapH_k, mapW_k, mapD_st, pb, sa_b, ca);
+    }
+    if (q.dH) {
+      if (!make_map(&mapD_k, dlog, V, cap, L.Vp * 2, BK, CM)) return FCKL_ERR_CUDA;
+      SchedArgs sa_h{SCHED_SPLIT_K, NTh, KBv, 0, 0, rc, 0, w3d, 0, narrow_h, 0, 2, 1,
+                     L.slab_units};
+      EpiCeDH::Params ph{H, invT, ctl};
+      ProfScope ps(K_DH, st, flops, 2.0 * nr * V + 2.0 * (double)V * H + 4.0 * nr * H);
+      FCKL_LAUNCH((gemm_pair_kernel<EpiCeDH, false, true>), 2 * pairs, GEMM_THREADS,
+                  pair_smem_bytes<EpiCeDH>(), mapD_k, mapW_mn, mapSlab, ph, sa_h, ca);
+    }
+    // dW (+)= dlogits^T h: dlogits and the gathered rows were complete before
+    // the dH GEMM launched, so its main loop starts at once (without a dH GEMM
+    // it follows the recompute GEMM directly).
+    if (q.dW) {
+      int d3d = 0, h3d = 0;
+      if (!make_map_mn(&mapD_mn, dlog, L.Vp, cap, L.Vp * 2, &d3d)) return FCKL_ERR_CUDA;
+      if (!make_map_mn(&mapH_mn, hst, H, cap, (long long)H * 2, &h3d)) return FCKL_ERR_CUDA;
+      const int MTv = (int)cdiv(V, PM);
+      SchedArgs sa_w{SCHED_TILES, NTh, 0, 1, MTv, rc, d3d, h3d, 0, narrow_h, q.dH ? 1 : 0};
+      ProfScope ps(K_DW, st, flops,
+                   2.0 * nr * (V + H) + (dw_direct16 ? 2.0 : c > 0 ? 8.0 : 4.0) * V * H);
+      if (dw_direct16) {
+        EpiCeDW::Params pw{V, H, invT, ctl};
+        FCKL_LAUNCH((gemm_pair_kernel<EpiCeDW, true, true>), grid_for((long long)MTv * NTh),
+                    GEMM_THREADS, pair_smem_bytes<EpiCeDW>(), mapD_mn, mapH_mn, mapdW, pw, sa_w,
+                    ca);
+      } else {
+        EpiCeDWSum::Params pw{V, H, invT, c > 0 ? 1 : 0, ctl};
+        FCKL_LAUNCH((gemm_pair_kernel<EpiCeDWSum, true, true>), grid_for((long long)MTv * NTh),
+                    GEMM_THREADS, pair_smem_bytes<EpiCeDWSum>(), mapD_mn, mapH_mn, mapdW, pw, sa_w, ca);
+      }
+    }
+    // the last chunk's blocks zero dW when no row was kept
+    const bool last = c + 1 == L.nchunks && q.dW && dw_dst == q.dW;
+    if (q.dH || last) {
+      uint4* zdw = last ? static_cast<uint4*>(q.dW) : nullptr;
+      const long long vecs = (long long)V * H * (bf16_grads ? 2 : 4) / 16;
+      ProfScope ps(K_DH_OUT, st, 0.0, nr * H * (bf16_grads ? 6.0 : 8.0));
+      if (bf16_grads)
+        FCKL_LAUNCH(k_ce_dh_out<__nv_bfloat16>, cap, 128, 0, (const float*)slab, clist, rc, H, NTh,
+                    KBv, pairs, L.slab_units, static_cast<__nv_bfloat16*>(q.dH), zdw, vecs,
+                    (const DeviceCtl*)ctl);
+      else
+        FCKL_LAUNCH(k_ce_dh_out<float>, cap, 128, 0, (const float*)slab, clist, rc, H, NTh, KBv,
+                    pairs, L.slab_units, static_cast<float*>(q.dH), zdw, vecs,
+                    (const DeviceCtl*)ctl);
+    }
+  }
+  if (q.dW && dw_dst != q.dW) {
+    const long long n4 = (long long)V * H / 4;
+    ProfScope ps(K_DW_OUT, st, 0.0, n4 * 24.0);
+    FCKL_LAUNCH(k_ce_dw_out, (int)std::min<long long>(cdiv(n4, 256), (long long)dev->sms * 8), 256,
+                0, (const float4*)dw_dst, n4, static_cast<uint2*>(q.dW), (const DeviceCtl*)ctl);
+  }
+  if (losses) {
+    ProfScope ps(K_FINAL, st, 0.0, (double)N * 4.0);
+    FCKL_LAUNCH(k_ce_finalize, 1, 1024, 0, (const float*)share, N, (const DeviceCtl*)ctl, q.loss);
+  }
+  return cudaGetLastError() == cudaSuccess ? FCKL_OK : FCKL_ERR_CUDA;
+}
+
+fckl_status run_ce(const CeRequest& q) {
+  const fckl_ce_problem* prob = q.prob;
+  const bool grads = q.mode != CeMode::kFwd;
+  if (!valid_ce(prob)) return FCKL_ERR_INVALID_ARG;
+  if (!q.hidden || !q.W || !q.labels || !aligned(q.hidden, 16) || !aligned(q.W, 16) ||
+      !aligned(q.labels, prob->label_type == FCKL_LABELS_LONG ? 8 : 4))
+    return FCKL_ERR_INVALID_ARG;
+  if (!aligned(q.factor, 4) || !aligned(q.row_loss, 4) || !aligned(q.lse_out, 4))
+    return FCKL_ERR_INVALID_ARG;
+  if (q.mode == CeMode::kBwd ? (!q.lse_in || !q.factor || !aligned(q.lse_in, 4))
+                             : (!q.loss || !aligned(q.loss, 4)))
+    return FCKL_ERR_INVALID_ARG;
+  if (grads && ((!q.dH && !q.dW) || !aligned(q.dH, 16) || !aligned(q.dW, 16)))
+    return FCKL_ERR_INVALID_ARG;
+  if (!supported_ce(prob)) return FCKL_ERR_UNSUPPORTED;
+  const CeLayout L = ce_layout(prob, grads);
+  if (q.workspace == nullptr || !aligned(q.workspace, kAlign) || q.ws_bytes < L.total)
+    return FCKL_ERR_WORKSPACE;
+  const CeDevice* dev = ce_device();
+  if (dev == nullptr || !dev->ok) return FCKL_ERR_UNSUPPORTED;
+  if (get_encode_fn() == nullptr) return FCKL_ERR_CUDA;
+  return prob->label_type == FCKL_LABELS_LONG ? enqueue_ce<int64_t>(q, L, dev)
+                                              : enqueue_ce<int32_t>(q, L, dev);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fckl_ce_workspace_bytes(const fckl_ce_problem* prob, int32_t gradients) {
+  if (!valid_ce(prob) || !supported_ce(prob)) return 0;
+  return ce_layout(prob, gradients != 0).total;
+}
+
+fckl_status fckl_ce_fwd(const fckl_ce_problem* prob, const void* hidden, const void* W,
+                        const void* labels, const float* row_weight, float* loss, float* row_loss,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  CeRequest q;
+  q.mode = CeMode::kFwd;
+  q.prob = prob; q.hidden = hidden; q.W = W; q.labels = labels; q.factor = row_weight;
+  q.loss = loss; q.row_loss = row_loss; q.lse_out = lse;
+  q.workspace = workspace; q.ws_bytes = workspace_bytes; q.stream = stream;
+  return run_ce(q);
+}
+
+fckl_status fckl_ce_fwd_bwd(const fckl_ce_problem* prob, const void* hidden, const void* W,
+                            const void* labels, const float* row_weight, float* loss,
+                            float* row_loss, float* lse, void* dH, void* dW, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  CeRequest q;
+  q.mode = CeMode::kFwdBwd;
+  q.prob = prob; q.hidden = hidden; q.W = W; q.labels = labels; q.factor = row_weight;
+  q.loss = loss; q.row_loss = row_loss; q.lse_out = lse; q.dH = dH; q.dW = dW;
+  q.workspace = workspace; q.ws_bytes = workspace_bytes; q.stream = stream;
+  return run_ce(q);
+}
+
+fckl_status fckl_ce_bwd(const fckl_ce_problem* prob, const void* hidden, const void* W,
+                        const void* labels, const float* lse, const float* row_grad, void* dH,
+                        void* dW, void* workspace, size_t workspace_bytes, void* stream) {
+  CeRequest q;
+  q.mode = CeMode::kBwd;
+  q.prob = prob; q.hidden = hidden; q.W = W; q.labels = labels; q.lse_in = lse;
+  q.factor = row_grad; q.dH = dH; q.dW = dW;
+  q.workspace = workspace; q.ws_bytes = workspace_bytes; q.stream = stream;
+  return run_ce(q);
+}
+
+fckl_status fckl_scale_gradient(void* grad, int64_t n, int32_t grad_type, const float* factor,
+                                void* stream) {
+  if (!grad || !factor || n < 1 || !aligned(grad, 16) || !aligned(factor, 4) ||
+      (grad_type != FCKL_GRAD_FLOAT && grad_type != FCKL_GRAD_BFLOAT))
+    return FCKL_ERR_INVALID_ARG;
+  const CeDevice* dev = ce_device();
+  if (dev == nullptr || !dev->ok) return FCKL_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int grid = (int)std::min<long long>(cdiv(cdiv(n, 4), 256), (long long)dev->sms * 8);
+  if (grad_type == FCKL_GRAD_BFLOAT)
+    k_scale<__nv_bfloat16><<<grid, 256, 0, st>>>(static_cast<__nv_bfloat16*>(grad), n, factor);
+  else
+    k_scale<float><<<grid, 256, 0, st>>>(static_cast<float*>(grad), n, factor);
+  return cudaGetLastError() == cudaSuccess ? FCKL_OK : FCKL_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -50,20 +50,7 @@ bool supported_problem(const fckl_problem* p) {
   return p->K <= FCKL_K_MAX && p->K <= p->V && p->H % 8 == 0;
 }
 
-long long resolve_chunk(const fckl_problem* p) {
-  const long long Vp = align_up((size_t)p->V, 64);
-  long long C = p->chunk;
-  if (C == 0) {
-    // 1 GiB of bf16 dlogits: at V = 128K a 4096-row chunk, deep enough that
-    // one dW read-modify-write (V*H*8 bytes) per chunk stays well under the
-    // chunk's dW tensor-core time, with few launches (and tail waves).
-    const long long budget = 1024ll << 20;
-    C = budget / (Vp * 2) / 128 * 128;
-    C = std::max(C, 128ll);
-    C = std::min(C, (long long)align_up((size_t)p->N, 64));
-  }
-  return std::min<long long>(C, p->N);
-}
+long long resolve_chunk(const fckl_problem* p) { return resolve_rows(p->N, p->V, p->chunk); }
 
 // full = false: the forward-loss-only layout (no dlogits, no entropy or
 // row-list buffers), used by the allocation-free entry point.
@@ -293,14 +280,6 @@ fckl_status run(const Request& q) {
   const float scale2 = 1.4426950408889634f / prob->T;
   CtlArgs ca{ctl, wait_timeout_ns(), debug_skip_commit()};
   const bool pdl = pdl_enabled();
-  // Launch with programmatic dependent launch; a failed launch ends the call.
-#define FCKL_LAUNCH(kernel, grid, block, smem, ...)                                   \
-  do {                                                                                 \
-    if (launch(pdl, kernel, (int)(grid), (int)(block), (size_t)(smem), st, __VA_ARGS__) != \
-        cudaSuccess)                                                                   \
-      return FCKL_ERR_CUDA;                                                            \
-  } while (0)
-
   if (cudaMemsetAsync(ctl, 0, sizeof(DeviceCtl), st) != cudaSuccess) return FCKL_ERR_CUDA;
   if (q.ready && cudaStreamWaitEvent(st, q.ready[0], 0) != cudaSuccess) return FCKL_ERR_CUDA;
   if (!ent) {
@@ -645,7 +624,6 @@ fckl_status run(const Request& q) {
     FCKL_LAUNCH(k_finalize, 1, 1024, 0, (const float*)rl, (long long)L.N, (const DeviceCtl*)ctl,
                 q.loss);
   }
-#undef FCKL_LAUNCH
   if (cudaGetLastError() != cudaSuccess) return FCKL_ERR_CUDA;
   return FCKL_OK;
 }

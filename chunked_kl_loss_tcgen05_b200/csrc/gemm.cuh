@@ -88,6 +88,7 @@ struct Work {
   int mt, nt;    // pair tile: rows [mt*256, +256), columns [nt*256, +256)
   int kb0, kb1;  // k-blocks [kb0, kb1) of 64
   int rev;       // 1: walk the k-blocks from kb1 - 1 down to kb0
+  int ks;        // k segment of the unit (SCHED_SPLIT_K; 0 otherwise)
   int m0, n0;    // this CTA's first row (mt*256 + 128*rank) and the first column
   int rows;      // rows of the launch (row-tiled kernels: rows >= rows are padding)
 };
@@ -131,6 +132,9 @@ struct SchedArgs {
   // touched last, which are still in L2 (the operand every wave re-reads is
   // then served mostly from L2 instead of DRAM).
   int serpentine;
+  // SCHED_SPLIT_K with S = 0, when every k segment is stored to a slab of its
+  // own: at most this many units (0: the partial tiles are added in place).
+  int slab_units;
 };
 
 __device__ __forceinline__ bool narrow_unit(const SchedArgs& a, const Work& w) {
@@ -140,16 +144,28 @@ __device__ __forceinline__ bool narrow_unit(const SchedArgs& a, const Work& w) {
 // Split-K factor for `tiles` output tiles of KB k-blocks on `slots` CTA pairs:
 // minimise waves * (k-blocks per unit + a fixed cost of 6 per unit).  Used on
 // the device when the row count (hence the tile count) is only known there;
-// the host applies the same model when it knows the rows.
-__device__ __forceinline__ int choose_split_dev(int tiles, int KB, int slots) {
+// the host applies the same model when it knows the rows.  With slab_units > 0
+// every segment is stored on its own and summed later, so a unit also costs
+// its 256 KB tile's way to L2 and back (about 1/8 of a k-block's time on all
+// pairs), and tiles * S stays within the slabs' room.  Called by a whole warp:
+// lane l weighs S = l + 1, l + 33, ...; ties go to the smallest S.
+__device__ __forceinline__ int choose_split_warp(int tiles, int KB, int slots, int slab_units) {
   if (tiles <= 0 || KB <= 0) return 1;
   int best = 1;
   long long best_cost = LLONG_MAX;
-  const int smax = KB < 128 ? KB : 128;
-  for (int S = 1; S <= smax; ++S) {
-    const long long waves = ((long long)tiles * S + slots - 1) / slots;
-    const long long cost = waves * ((KB + S - 1) / S + 6);
+  int smax = KB < 128 ? KB : 128;
+  if (slab_units > 0) smax = min(smax, max(1, slab_units / tiles));
+  for (int S = (threadIdx.x & 31) + 1; S <= smax; S += 32) {
+    const int waves = (int)(((long long)tiles * S + slots - 1) / slots);
+    const long long cost = 8ll * waves * ((KB + S - 1) / S + 6) +
+                           (slab_units > 0 ? (long long)tiles * S : 0);
     if (cost < best_cost) { best_cost = cost; best = S; }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const long long c = __shfl_xor_sync(0xffffffffu, best_cost, o);
+    const int b = __shfl_xor_sync(0xffffffffu, best, o);
+    if (c < best_cost || (c == best_cost && b < best)) { best_cost = c; best = b; }
   }
   return best;
 }
@@ -182,7 +198,7 @@ struct PairSched {
     if (a.kind == SCHED_VOCAB_MAJOR) {
       w.nt = (int)(u / MT);
       w.mt = (int)(u - (long long)w.nt * MT);
-      w.kb0 = 0; w.kb1 = KB; w.rev = 0;
+      w.kb0 = 0; w.kb1 = KB; w.rev = 0; w.ks = 0;
     } else if (a.kind == SCHED_SPLIT_K) {
       const int ks = (int)(u / tiles);
       const int tile = (int)(u - (long long)ks * tiles);
@@ -193,12 +209,13 @@ struct PairSched {
       }
       w.kb0 = (int)((long long)ks * KB / a.S);
       w.kb1 = (int)((long long)(ks + 1) * KB / a.S);
+      w.ks = ks;
       w.rev = a.serpentine ? (int)((u / G) & 1) : 0;  // odd waves walk backwards
     } else {
       const int t = (int)(u / a.NT);
       w.nt = (int)(u - (long long)t * a.NT);
       w.mt = a.mt0 + t;
-      w.kb0 = 0; w.kb1 = KB; w.rev = 0;
+      w.kb0 = 0; w.kb1 = KB; w.rev = 0; w.ks = 0;
     }
     w.rows = rows;
     u += G;
@@ -251,6 +268,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
   const int cluster = blockIdx.x >> 1;
   const int nclusters = gridDim.x >> 1;
 
+  if (warp == 0) {
+    // Split-K factor chosen here when only the device knows the rows; every
+    // role (and both CTAs of the pair, from the same inputs) uses this value.
+    const int S = (sa.kind == SCHED_SPLIT_K && sa.S == 0)
+                      ? choose_split_warp(((sa.rc.get() + PM - 1) / PM) * sa.NT, sa.KB, nclusters,
+                                          sa.slab_units)
+                      : sa.S;
+    if (lane == 0) *split_slot = S;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -262,11 +288,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0u;
-    // Split-K factor chosen here when only the device knows the rows; every
-    // role (and both CTAs of the pair, from the same inputs) uses this value.
-    *split_slot = (sa.kind == SCHED_SPLIT_K && sa.S == 0)
-                      ? choose_split_dev(((sa.rc.get() + PM - 1) / PM) * sa.NT, sa.KB, nclusters)
-                      : sa.S;
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);

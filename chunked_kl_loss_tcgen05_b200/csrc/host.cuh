@@ -12,6 +12,7 @@
 #include <utility>
 #include <vector>
 
+#include "fckl.h"
 #include "gemm.cuh"
 
 namespace fckl {
@@ -23,6 +24,23 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Rows per chunk: the caller's (0: the largest multiple of 128 rows whose
+// 16-bit [rows, V] block, V padded to 64 columns, fits in 1 GiB -- at V = 128K
+// a 4096-row chunk, deep enough that one dW read-modify-write (V*H*8 bytes) per
+// chunk stays well under the chunk's dW tensor-core time, with few launches and
+// tail waves), at most N.
+inline long long resolve_rows(long long N, long long V, long long chunk) {
+  long long C = chunk;
+  if (C == 0) {
+    const long long budget = 1024ll << 20;
+    C = budget / ((long long)align_up((size_t)V, 64) * 2) / 128 * 128;
+    if (C < 128) C = 128;
+    const long long Nr = (long long)align_up((size_t)N, 64);
+    if (C > Nr) C = Nr;
+  }
+  return C < N ? C : N;
+}
 
 // ---------------------------------------------------------------- tensor maps
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -125,15 +143,24 @@ cudaError_t launch(bool pdl, void (*kernel)(KArgs...), int grid, int block, size
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// Ends the enclosing call with FCKL_ERR_CUDA when the launch fails.
+#define FCKL_LAUNCH(kernel, grid, block, smem, ...)                                          \
+  do {                                                                                       \
+    if (::fckl::launch(pdl, kernel, (int)(grid), (int)(block), (size_t)(smem), st, __VA_ARGS__) != \
+        cudaSuccess)                                                                         \
+      return FCKL_ERR_CUDA;                                                                  \
+  } while (0)
+
 // ---------------------------------------------------------------- profiling
 enum Kind {
   K_COUNT, K_PREP, K_FWD, K_MERGE, K_BWD, K_DH, K_DW, K_FINAL, K_ENT, K_ENT_MERGE, K_GATHER,
-  K_SCATTER, K_SELECT, K_ZERO_DW, K_NKINDS
+  K_SCATTER, K_SELECT, K_ZERO_DW, K_CE_FWD, K_CE_DLOGITS, K_DH_OUT, K_DW_OUT, K_NKINDS
 };
 inline const char* const kKindName[K_NKINDS] = {
     "count_valid", "prep_teacher", "fwd_logits_lse", "merge_loss", "bwd_dlogits",
     "dH_gemm",     "dW_gemm",      "finalize",       "entropy_gemm", "merge_entropy",
-    "gather_rows", "scatter_rows", "select_rows", "zero_dw"};
+    "gather_rows", "scatter_rows", "select_rows", "zero_dw", "ce_logits", "ce_dlogits",
+    "dH_rows", "dW_round"};
 struct ProfRec {
   int kind;
   cudaEvent_t a, b;

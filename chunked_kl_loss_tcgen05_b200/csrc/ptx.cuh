@@ -97,7 +97,7 @@ __device__ __forceinline__ void raise_timeout(const WaitCtx& w, uint32_t site) {
 // CTA has already aborted.  Never spins without limit.  sleep_ns > 0: sleep
 // between polls (for waits that last many microseconds and can afford the
 // extra latency; fewer issued polls save power under the power cap).
-__device__ __noinline__ bool wait_phase_slow(uint32_t bar, uint32_t parity, const WaitCtx& w,
+static __device__ __noinline__ bool wait_phase_slow(uint32_t bar, uint32_t parity, const WaitCtx& w,
                                              uint32_t site, uint32_t sleep_ns) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
@@ -123,7 +123,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
 
 // Cleanup wait: ignores the abort flag (it is used to let in-flight copies and
 // MMAs land before the CTA exits), bounded by the same budget.
-__device__ __noinline__ bool drain_phase(uint32_t bar, uint32_t parity, const WaitCtx& w,
+static __device__ __noinline__ bool drain_phase(uint32_t bar, uint32_t parity, const WaitCtx& w,
                                          uint32_t site) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 0;; ++it) {

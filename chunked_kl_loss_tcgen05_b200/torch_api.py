@@ -10,15 +10,18 @@ from __future__ import annotations
 
 import torch
 
-from . import (FcklError, FcklProblem, FCKL_OK, fckl_check, fckl_fwd, fckl_fwd_bwd,
-               fckl_fwd_bwd_host, fckl_fwd_bwd_sliced, fckl_host_workspace_bytes,
-               fckl_workspace_bytes)
+from . import (FcklCeProblem, FcklError, FcklProblem, FCKL_GRAD_BFLOAT, FCKL_GRAD_FLOAT,
+               FCKL_LABELS_INT, FCKL_LABELS_LONG, FCKL_OK, FCKL_REDUCE_MEAN, FCKL_REDUCE_SUM,
+               fckl_ce_bwd, fckl_ce_fwd, fckl_ce_fwd_bwd, fckl_ce_workspace_bytes, fckl_check,
+               fckl_fwd, fckl_fwd_bwd, fckl_fwd_bwd_host, fckl_fwd_bwd_sliced,
+               fckl_host_workspace_bytes, fckl_scale_gradient, fckl_workspace_bytes)
 
 __all__ = ["make_problem", "alloc_workspace", "fused_kl_fwd", "fused_kl_fwd_bwd", "student_entropy",
            "select_top_rows", "fused_kl_rows", "arrays_to_device",
            "fused_kl_from_host", "alloc_host_workspace", "fused_kl_fwd_bwd_host",
            "fused_kl_fwd_bwd_sliced",
-           "FusedChunkedKL", "fused_chunked_kl_loss"]
+           "FusedChunkedKL", "fused_chunked_kl_loss", "fused_ce_fwd", "fused_ce_fwd_bwd",
+           "fused_ce_bwd", "FusedCrossEntropy", "fused_cross_entropy_loss"]
 
 
 def _bits(t: torch.Tensor) -> torch.Tensor:
@@ -379,3 +382,243 @@ def fused_kl_rows(hidden, W, topk_idx, topk_logit, rows, T=1.0, chunk=0, workspa
         if st != FCKL_OK:
             raise FcklError(st, "fckl_check")
     return loss, row_loss, dH, dW
+
+
+# ---------------------------------------------------------------- cross entropy
+_REDUCTIONS = {"mean": FCKL_REDUCE_MEAN, "sum": FCKL_REDUCE_SUM}
+_GRAD_TYPES = {torch.float32: FCKL_GRAD_FLOAT, torch.bfloat16: FCKL_GRAD_BFLOAT}
+_LABEL_TYPES = {torch.int32: FCKL_LABELS_INT, torch.int64: FCKL_LABELS_LONG}
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _ce_setup(hidden, W, labels, rows, T, label_smoothing, z_loss, ignore_index, reduction, chunk,
+              n_valid_total, grad_dtype, workspace, gradients):
+    """Checks, the problem and the workspace of a cross-entropy call.  ``rows``:
+    (name, tensor or None) of the per-row float32 inputs."""
+    hidden, W = _bits(hidden), _bits(W)
+    _check_shapes(hidden, W)
+    N, H = hidden.shape
+    if labels.dtype not in _LABEL_TYPES:
+        raise TypeError(f"labels must be int32 or int64, got {labels.dtype}")
+    if labels.dim() != 1 or labels.shape[0] != N:
+        raise ValueError(f"labels must be [N={N}], got {tuple(labels.shape)}")
+    for name, t in rows:
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (N,)):
+            raise TypeError(f"{name} must be a float32 tensor [N={N}]")
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}, got {reduction!r}")
+    if grad_dtype not in _GRAD_TYPES:
+        raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
+    _check_placement(True, [("hidden", hidden), ("W", W), ("labels", labels)] + list(rows))
+    prob = FcklCeProblem(N, H, W.shape[0], T, label_smoothing, z_loss, _REDUCTIONS[reduction],
+                         ignore_index, chunk, n_valid_total, _LABEL_TYPES[labels.dtype],
+                         _GRAD_TYPES[grad_dtype])
+    dev = hidden.device
+    if workspace is None:
+        nbytes = fckl_ce_workspace_bytes(prob, gradients)
+        if nbytes == 0:
+            raise FcklError(1, "fckl_ce_workspace_bytes")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
+          or workspace.device != dev):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    return hidden, W, prob, workspace
+
+
+def _check_grad_out(name, t, shape, dtype, device):
+    if (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()
+            or t.device != device):
+        raise ValueError(f"out {name} must be a contiguous {dtype} tensor {shape} on {device}")
+
+
+def _finish(status, where, workspace, stream, check):
+    if status == FCKL_OK and check:
+        where, status = "fckl_check", fckl_check(workspace.data_ptr(), stream)
+    if status != FCKL_OK:
+        raise FcklError(status, where)
+
+
+def fused_ce_fwd(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0, z_loss=0.0,
+                 ignore_index=-100, reduction="mean", chunk=0, workspace=None, check=True,
+                 n_valid_total=0):
+    """Cross entropy of softmax(hidden W^T / T) against ``labels`` (int32 or int64
+    [N]; rows whose label is ``ignore_index`` are left out).  Returns (loss[1],
+    row_loss[N], lse[N]), float32; row_loss is without ``row_weight`` (float32
+    [N], the rows' weights in ``loss``).  ``reduction``: "mean" over the rows
+    that count (``n_valid_total`` > 0 replaces their number) or "sum"."""
+    hidden, W, prob, workspace = _ce_setup(hidden, W, labels, (("row_weight", row_weight),), T,
+                                           label_smoothing, z_loss, ignore_index, reduction, chunk,
+                                           n_valid_total, torch.float32, workspace, False)
+    dev = hidden.device
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    row_loss = torch.empty(prob.N, dtype=torch.float32, device=dev)
+    lse = torch.empty(prob.N, dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        st = fckl_ce_fwd(prob, hidden.data_ptr(), W.data_ptr(), labels.data_ptr(),
+                         _ptr(row_weight), loss.data_ptr(), row_loss.data_ptr(), lse.data_ptr(),
+                         workspace.data_ptr(), workspace.numel(), stream)
+        _finish(st, "fckl_ce_fwd", workspace, stream, check)
+    return loss, row_loss, lse
+
+
+def _fused_ce_fwd_bwd(hidden, W, labels, row_weight, T, label_smoothing, z_loss, ignore_index,
+                      reduction, chunk, workspace, check, out, grad_dtype, n_valid_total,
+                      want=(True, True), want_lse=False):
+    hidden, W, prob, workspace = _ce_setup(hidden, W, labels, (("row_weight", row_weight),), T,
+                                           label_smoothing, z_loss, ignore_index, reduction, chunk,
+                                           n_valid_total, grad_dtype, workspace, True)
+    dev = hidden.device
+    if out is not None:
+        if len(out) != 3:
+            raise ValueError("out must be (loss, dH, dW)")
+        loss, dH, dW = out
+        _check_grad_out("loss", loss, (1,), torch.float32, dev)
+        _check_grad_out("dH", dH, (prob.N, prob.H), grad_dtype, dev)
+        _check_grad_out("dW", dW, (prob.V, prob.H), grad_dtype, dev)
+    else:
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        dH = torch.empty(prob.N, prob.H, dtype=grad_dtype, device=dev) if want[0] else None
+        dW = torch.empty(prob.V, prob.H, dtype=grad_dtype, device=dev) if want[1] else None
+    row_loss = torch.empty(prob.N, dtype=torch.float32, device=dev)
+    lse = torch.empty(prob.N, dtype=torch.float32, device=dev) if want_lse else None
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        st = fckl_ce_fwd_bwd(prob, hidden.data_ptr(), W.data_ptr(), labels.data_ptr(),
+                             _ptr(row_weight), loss.data_ptr(), row_loss.data_ptr(), _ptr(lse),
+                             _ptr(dH), _ptr(dW), workspace.data_ptr(), workspace.numel(), stream)
+        _finish(st, "fckl_ce_fwd_bwd", workspace, stream, check)
+    return loss, row_loss, lse, dH, dW
+
+
+def fused_ce_fwd_bwd(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0, z_loss=0.0,
+                     ignore_index=-100, reduction="mean", chunk=0, workspace=None, check=True,
+                     out=None, grad_dtype=torch.float32, n_valid_total=0):
+    """fused_ce_fwd with the gradients of ``loss`` in the same call: returns
+    (loss[1], row_loss[N], dH[N,H], dW[V,H]), the gradients in ``grad_dtype``
+    (float32 or bfloat16).  ``out``: optional (loss, dH, dW) to write into."""
+    loss, row_loss, _, dH, dW = _fused_ce_fwd_bwd(
+        hidden, W, labels, row_weight, T, label_smoothing, z_loss, ignore_index, reduction, chunk,
+        workspace, check, out, grad_dtype, n_valid_total)
+    return loss, row_loss, dH, dW
+
+
+def fused_ce_bwd(hidden, W, labels, lse, row_grad, T=1.0, label_smoothing=0.0, z_loss=0.0,
+                 ignore_index=-100, chunk=0, workspace=None, check=True, out=None,
+                 grad_dtype=torch.float32, want=(True, True)):
+    """Gradients of sum(row_grad * row_loss) for the row losses and ``lse`` that
+    fused_ce_fwd returned on the same inputs; row_grad float32 [N], of either
+    sign.  Returns (dH[N,H], dW[V,H]); ``want`` = (dH, dW): leave one out (None)."""
+    if lse is None or row_grad is None:
+        raise TypeError("lse and row_grad must be float32 tensors [N]")
+    if not any(want):
+        raise ValueError("want leaves out both gradients")
+    hidden, W, prob, workspace = _ce_setup(hidden, W, labels,
+                                           (("lse", lse), ("row_grad", row_grad)), T,
+                                           label_smoothing, z_loss, ignore_index, "sum", chunk, 0,
+                                           grad_dtype, workspace, True)
+    dev = hidden.device
+    if out is not None:
+        if len(out) != 2:
+            raise ValueError("out must be (dH, dW)")
+        dH, dW = out
+        _check_grad_out("dH", dH, (prob.N, prob.H), grad_dtype, dev)
+        _check_grad_out("dW", dW, (prob.V, prob.H), grad_dtype, dev)
+    else:
+        dH = torch.empty(prob.N, prob.H, dtype=grad_dtype, device=dev) if want[0] else None
+        dW = torch.empty(prob.V, prob.H, dtype=grad_dtype, device=dev) if want[1] else None
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        st = fckl_ce_bwd(prob, hidden.data_ptr(), W.data_ptr(), labels.data_ptr(), lse.data_ptr(),
+                         row_grad.data_ptr(), _ptr(dH), _ptr(dW), workspace.data_ptr(),
+                         workspace.numel(), stream)
+        _finish(st, "fckl_ce_bwd", workspace, stream, check)
+    return dH, dW
+
+
+def _scale_gradient(t, factor):
+    """t *= factor (a device float32 scalar) in place; free when the factor is 1."""
+    if t is None:
+        return
+    with torch.cuda.device(t.device):
+        st = fckl_scale_gradient(t.data_ptr(), t.numel(), _GRAD_TYPES[t.dtype], factor.data_ptr(),
+                                 torch.cuda.current_stream(t.device).cuda_stream)
+    if st != FCKL_OK:
+        raise FcklError(st, "fckl_scale_gradient")
+
+
+class FusedCrossEntropy(torch.autograd.Function):
+    """Cross entropy with gradients for hidden and W, in their own dtype (bf16).
+
+    reduction "mean" / "sum": the fused call computes the gradients in forward;
+    the first backward multiplies them by the upstream factor (rounded once more
+    unless it is a power of two) and hands them over, later ones (retain_graph)
+    compute them again from the saved log-sum-exps.  reduction "none": forward
+    returns the row losses, backward computes the gradients for the given
+    upstream gradient."""
+
+    @staticmethod
+    def forward(ctx, hidden, W, labels, row_weight, reduction, ignore_index, check, opts):
+        want = ctx.needs_input_grad[:2]
+        ctx.set_materialize_grads(False)
+        ctx.reduction, ctx.ignore_index, ctx.check, ctx.opts = reduction, ignore_index, check, opts
+        ctx.want, ctx.grads = want, None
+        kw = dict(ignore_index=ignore_index, check=check, **opts)
+        if reduction == "none":
+            if row_weight is not None:
+                raise ValueError('row_weight needs reduction "mean" or "sum"')
+            _, value, lse = fused_ce_fwd(hidden, W, labels, reduction="sum", **kw)
+        elif any(want):
+            loss, _, lse, dH, dW = _fused_ce_fwd_bwd(
+                hidden, W, labels, row_weight, reduction=reduction, workspace=None, out=None,
+                grad_dtype=torch.bfloat16, n_valid_total=0, want=want, want_lse=True, **kw)
+            ctx.grads = (dH, dW)
+            value = loss[0]
+        else:
+            loss, _, lse = fused_ce_fwd(hidden, W, labels, row_weight, reduction=reduction, **kw)
+            value = loss[0]
+        ctx.save_for_backward(hidden, W, labels, row_weight, lse)
+        return value
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        none = (None,) * 6
+        if grad_out is None:
+            return (None, None) + none
+        hidden, W, labels, row_weight, lse = ctx.saved_tensors
+        if ctx.grads is not None:
+            (dH, dW), ctx.grads = ctx.grads, None
+            for t in (dH, dW):
+                _scale_gradient(t, grad_out)
+            return (dH, dW) + none
+        row_grad = grad_out
+        if ctx.reduction != "none":
+            row_grad = grad_out.expand(labels.shape[0])
+            if row_weight is not None:
+                row_grad = row_grad * row_weight
+            if ctx.reduction == "mean":
+                V = W.shape[0]
+                kept = (labels != ctx.ignore_index) & (labels >= 0) & (labels < V)
+                row_grad = row_grad / kept.sum().clamp(min=1)
+        dH, dW = fused_ce_bwd(hidden, W, labels, lse, row_grad.contiguous(),
+                              ignore_index=ctx.ignore_index, check=ctx.check,
+                              grad_dtype=torch.bfloat16, want=ctx.want, **ctx.opts)
+        return (dH, dW) + none
+
+
+def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0,
+                             z_loss=0.0, ignore_index=-100, reduction="mean", chunk=0, check=True):
+    """Differentiable fused_ce_fwd: the loss (a scalar), or with reduction "none"
+    the row losses [N].  hidden and W are bfloat16; ``row_weight`` gets no
+    gradient.  ``check=False`` leaves out the device-error check, which
+    synchronises the stream."""
+    if row_weight is not None and row_weight.requires_grad:
+        raise ValueError("row_weight gets no gradient; detach it")
+    if reduction not in ("mean", "sum", "none"):
+        raise ValueError(f'reduction must be "mean", "sum" or "none", got {reduction!r}')
+    opts = dict(T=T, label_smoothing=label_smoothing, z_loss=z_loss, chunk=chunk)
+    return FusedCrossEntropy.apply(hidden, W, labels, row_weight, reduction, ignore_index, check,
+                                   opts)

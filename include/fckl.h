@@ -301,6 +301,78 @@ fckl_status fckl_fwd_bwd_rows(const fckl_problem* prob, const void* hidden, cons
                               float* dH, float* dW, void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* ----------------------------------------------------------------------------
+ * Cross entropy against labels over the same fused projection (the hard-label
+ * loss of the student head, next to the distillation loss; an addition of this
+ * library):
+ *   a = W h_r / T,  q = softmax(a) over all V,  LSE = log sum_v exp a_v
+ *   l_r  = (1 - e)(LSE - a_y) + e (LSE - mean_v a_v) + lam LSE^2
+ *   loss = (1/D) sum_r w_r l_r over the rows whose label y is not ignore_index;
+ *          D = their number (mean) or 1 (sum); 0 when there is none
+ *   d l_r / d a = q (1 + 2 lam LSE) - (1 - e) 1_y - e / V
+ * with e = label_smoothing, lam = z_loss, w = row_weight.  The [N, V] logits
+ * are never written: the vocabulary is walked in tiles of 256 columns whose
+ * log-sum-exp partials leave the GEMM epilogue, and the backward's bf16
+ * [chunk, V] block of dlogits bounds the workspace.
+ * Rows that are left out (ignore_index) cost no GEMM work and their hidden
+ * rows, weights and gradients are not read; row_loss, lse and dH are 0 there.
+ * A label outside [0, V) that is not ignore_index leaves its row out and is
+ * reported by fckl_check() as FCKL_ERR_BAD_INDEX.
+ * hidden, W, alignment, streams, workspace and errors are as above (H % 8 == 0).
+ * Repeated calls on the same inputs give the same bits.
+ * ------------------------------------------------------------------------- */
+typedef enum { FCKL_REDUCE_MEAN = 0, FCKL_REDUCE_SUM = 1 } fckl_reduction;
+typedef enum { FCKL_LABELS_INT = 0, FCKL_LABELS_LONG = 1 } fckl_label_type; /* int32, int64 */
+typedef enum { FCKL_GRAD_FLOAT = 0, FCKL_GRAD_BFLOAT = 1 } fckl_grad_type;  /* fp32, bf16   */
+
+typedef struct {
+  int64_t N;             /* rows                                              */
+  int64_t H;             /* hidden size, H % 8 == 0                           */
+  int64_t V;             /* vocabulary size                                   */
+  float T;               /* temperature (> 0): logits are W h / T             */
+  float label_smoothing; /* e, 0 <= e <= 1                                    */
+  float z_loss;          /* lam >= 0                                          */
+  int32_t reduction;     /* fckl_reduction                                    */
+  int64_t ignore_index;  /* label of rows that do not count                   */
+  int64_t chunk;         /* rows per chunk, 0 = automatic (as fckl_problem)   */
+  int64_t n_valid_total; /* mean: > 0 replaces the number of kept rows as D   */
+  int32_t label_type;    /* fckl_label_type of labels                         */
+  int32_t grad_type;     /* fckl_grad_type of dH and dW                       */
+} fckl_ce_problem;
+
+/* Device workspace in bytes (0 when the problem is invalid): gradients = 0 for
+ * fckl_ce_fwd, 1 for fckl_ce_fwd_bwd and fckl_ce_bwd.  With gradients it holds
+ * one chunk's bf16 [chunk, V] block, one chunk's gathered rows and fp32 dH
+ * partials, and, for bf16 gradients of several chunks, the fp32 sum of dW. */
+size_t fckl_ce_workspace_bytes(const fckl_ce_problem* prob, int32_t gradients);
+
+/* Loss, and optionally row_loss [N] (l_r, without the weight) and lse [N]
+ * (natural log).  row_weight [N] fp32 or NULL (ones).  2*H*V flops per kept row. */
+fckl_status fckl_ce_fwd(const fckl_ce_problem* prob, const void* hidden, const void* W,
+                        const void* labels, const float* row_weight, float* loss, float* row_loss,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Forward and backward in one call: dH [N, H] and dW [V, H] of `loss`, in
+ * grad_type, overwritten.  row_loss and lse may be NULL, and so may one of dH
+ * and dW (a frozen projection, or frozen rows: that product is not computed). */
+fckl_status fckl_ce_fwd_bwd(const fckl_ce_problem* prob, const void* hidden, const void* W,
+                            const void* labels, const float* row_weight, float* loss,
+                            float* row_loss, float* lse, void* dH, void* dW, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Backward of the row losses: dH and dW of sum_r row_grad[r] l_r, for the lse
+ * [N] that fckl_ce_fwd wrote for the same inputs (reduction and n_valid_total
+ * take no part).  One of dH and dW may be NULL.  6*H*V flops per kept row. */
+fckl_status fckl_ce_bwd(const fckl_ce_problem* prob, const void* hidden, const void* W,
+                        const void* labels, const float* lse, const float* row_grad, void* dH,
+                        void* dW, void* workspace, size_t workspace_bytes, void* stream);
+
+/* grad[0, n) (grad_type elements, 16-byte aligned) *= *factor in place, for a
+ * gradient that was computed before its upstream factor (device fp32 scalar)
+ * was known.  A factor of exactly 1 reads and writes nothing but the factor. */
+fckl_status fckl_scale_gradient(void* grad, int64_t n, int32_t grad_type, const float* factor,
+                                void* stream);
+
 /* Synchronises `stream`, then returns the first device-side error recorded in
  * `workspace` by the last call that used it (FCKL_OK if none), or
  * FCKL_ERR_CUDA if the stream reports a CUDA error. */
@@ -327,7 +399,8 @@ const char* fckl_status_string(fckl_status status);
  *        4 bwd_dlogits, 5 dH_gemm, 6 dW_gemm, 7 finalize, 8 entropy_gemm,
  *        9 merge_entropy, 10 gather_rows, 11 scatter_rows (reserved: gathered
  *        rows write their results in place, no kernel of this kind runs),
- *        12 select_rows, 13 zero_dw. */
+ *        12 select_rows, 13 zero_dw, 14 ce_logits, 15 ce_dlogits, 16 dH_rows,
+ *        17 dW_round. */
 typedef struct {
   char name[32];     /* kernel kind, e.g. "fwd_logits_lse" */
   int64_t launches;  /* launches recorded */

@@ -21,3 +21,4 @@ from .kl import (  # noqa: F401
     oracle_from_inputs,
 )
 from .selective import student_entropy, select_top_rows  # noqa: F401
+from .cross_entropy import cross_entropy  # noqa: F401
