@@ -25,6 +25,8 @@ __all__ = [
     "FcklCeProblem", "FCKL_REDUCE_MEAN", "FCKL_REDUCE_SUM", "FCKL_LABELS_INT", "FCKL_LABELS_LONG",
     "FCKL_GRAD_FLOAT", "FCKL_GRAD_BFLOAT", "fckl_ce_workspace_bytes", "fckl_ce_fwd",
     "fckl_ce_fwd_bwd", "fckl_ce_bwd", "fckl_scale_gradient",
+    "FcklNormProblem", "FCKL_FLOAT", "FCKL_BFLOAT", "FCKL_NORM_POST", "FCKL_NORM_PRE",
+    "fckl_block_norm_workspace_bytes", "fckl_block_norm_fwd", "fckl_block_norm_bwd",
 ]
 
 FCKL_OK = 0
@@ -45,7 +47,9 @@ exported_symbols = ("fckl_workspace_bytes", "fckl_resolved_chunk", "fckl_fwd", "
                     "fckl_fwd_noalloc", "fckl_student_entropy", "fckl_select_top_rows",
                     "fckl_fwd_bwd_rows", "fckl_host_workspace_bytes", "fckl_fwd_bwd_host",
                     "fckl_fwd_bwd_sliced", "fckl_ce_workspace_bytes", "fckl_ce_fwd",
-                    "fckl_ce_fwd_bwd", "fckl_ce_bwd", "fckl_scale_gradient")
+                    "fckl_ce_fwd_bwd", "fckl_ce_bwd", "fckl_scale_gradient",
+                    "fckl_block_norm_workspace_bytes", "fckl_block_norm_fwd",
+                    "fckl_block_norm_bwd")
 
 
 FCKL_TEACHER_LOGITS = 0
@@ -53,6 +57,8 @@ FCKL_TEACHER_PROBS = 1
 FCKL_REDUCE_MEAN, FCKL_REDUCE_SUM = 0, 1
 FCKL_LABELS_INT, FCKL_LABELS_LONG = 0, 1
 FCKL_GRAD_FLOAT, FCKL_GRAD_BFLOAT = 0, 1
+FCKL_FLOAT, FCKL_BFLOAT = 0, 1
+FCKL_NORM_POST, FCKL_NORM_PRE = 1, 2
 
 
 class FcklProblem(ctypes.Structure):
@@ -83,6 +89,20 @@ class FcklCeProblem(ctypes.Structure):
         super().__init__(int(N), int(H), int(V), float(T), float(label_smoothing), float(z_loss),
                          int(reduction), int(ignore_index), int(chunk), int(n_valid_total),
                          int(label_type), int(grad_type))
+
+
+class FcklNormProblem(ctypes.Structure):
+    """Mirror of ``fckl_norm_problem``."""
+    _fields_ = [("N", ctypes.c_int64), ("H", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("flags", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("weight_type", ctypes.c_int32), ("dy_type", ctypes.c_int32)]
+
+    def __init__(self, N, H, scale=1.0, eps=1e-6, weight_offset=0.0,
+                 flags=FCKL_NORM_POST | FCKL_NORM_PRE, x_type=FCKL_BFLOAT,
+                 weight_type=FCKL_BFLOAT, dy_type=FCKL_BFLOAT):
+        super().__init__(int(N), int(H), float(scale), float(eps), float(weight_offset),
+                         int(flags), int(x_type), int(weight_type), int(dy_type))
 
 
 class FcklKernelStat(ctypes.Structure):
@@ -154,6 +174,13 @@ def load() -> ctypes.CDLL:
     lib.fckl_ce_bwd.restype = ctypes.c_int
     lib.fckl_scale_gradient.argtypes = [vp, ctypes.c_int64, i32, vp, vp]
     lib.fckl_scale_gradient.restype = ctypes.c_int
+    M = ctypes.POINTER(FcklNormProblem)
+    lib.fckl_block_norm_workspace_bytes.argtypes = [M]
+    lib.fckl_block_norm_workspace_bytes.restype = sz
+    lib.fckl_block_norm_fwd.argtypes = [M] + [vp] * 8
+    lib.fckl_block_norm_fwd.restype = ctypes.c_int
+    lib.fckl_block_norm_bwd.argtypes = [M] + [vp] * 12 + [vp, sz, vp]
+    lib.fckl_block_norm_bwd.restype = ctypes.c_int
     lib.fckl_profile_begin.argtypes = [ctypes.c_uint32]
     lib.fckl_profile_begin.restype = None
     lib.fckl_profile_end.argtypes = [ctypes.POINTER(FcklKernelStat), ctypes.c_int]
@@ -284,6 +311,25 @@ def fckl_scale_gradient(grad, n, grad_type, factor, stream) -> int:
     return load().fckl_scale_gradient(grad, n, grad_type, factor, stream)
 
 
+def fckl_block_norm_workspace_bytes(prob: FcklNormProblem) -> int:
+    return int(load().fckl_block_norm_workspace_bytes(ctypes.byref(prob)))
+
+
+def fckl_block_norm_fwd(prob, x, block, post_weight, gate, pre_weight, v, y, stream) -> int:
+    """Array arguments are device addresses (ints) or None; returns the status."""
+    return load().fckl_block_norm_fwd(ctypes.byref(prob), x, block, post_weight, gate, pre_weight,
+                                      v, y, stream)
+
+
+def fckl_block_norm_bwd(prob, x, block, post_weight, gate, pre_weight, dy, dv, dx, dblock,
+                        dpost_weight, dgate, dpre_weight, workspace, workspace_bytes,
+                        stream) -> int:
+    """Array arguments are device addresses (ints) or None; returns the status."""
+    return load().fckl_block_norm_bwd(ctypes.byref(prob), x, block, post_weight, gate, pre_weight,
+                                      dy, dv, dx, dblock, dpost_weight, dgate, dpre_weight,
+                                      workspace, workspace_bytes, stream)
+
+
 def fckl_check(workspace, stream) -> int:
     return int(load().fckl_check(_ptr(workspace), _ptr(stream)))
 
@@ -295,7 +341,7 @@ def fckl_status_string(status: int) -> str:
 KERNEL_KINDS = ("count_valid", "prep_teacher", "fwd_logits_lse", "merge_loss", "bwd_dlogits",
                 "dH_gemm", "dW_gemm", "finalize", "entropy_gemm", "merge_entropy", "gather_rows",
                 "scatter_rows", "select_rows", "zero_dw", "ce_logits", "ce_dlogits", "dH_rows",
-                "dW_round")
+                "dW_round", "norm_fwd", "norm_bwd", "norm_sum")
 
 
 def fckl_profile_begin(kinds=None) -> None:

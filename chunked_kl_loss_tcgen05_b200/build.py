@@ -11,9 +11,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfckl.so")
-SOURCES = ["fckl.cu", "ce.cu"]
-HEADERS = ["ptx.cuh", "reduce.cuh", "gemm.cuh", "epilogues.cuh", "rows.cuh", "ce.cuh",
-           "host.cuh"]
+SOURCES = ["fckl.cu", "ce.cu", "norm.cu"]
+HEADERS = ["ptx.cuh", "vec.cuh", "reduce.cuh", "gemm.cuh", "epilogues.cuh", "rows.cuh", "ce.cuh",
+           "norm.cuh", "host.cuh"]
 
 
 def nvcc_path() -> str:

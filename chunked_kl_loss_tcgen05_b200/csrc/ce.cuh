@@ -460,11 +460,6 @@ __global__ void __launch_bounds__(1024) k_ce_finalize(const float* __restrict__ 
   }
 }
 
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
-
 // dH rows of one chunk: the sum of the row's slabs, in segment order, to the
 // caller's row (zeros for left-out rows), rounded once.  One block per list
 // entry.  The number of segments is the one the dH GEMM chose (same inputs).

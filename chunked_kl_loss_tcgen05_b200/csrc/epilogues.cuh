@@ -30,6 +30,7 @@
 #include <climits>
 
 #include "gemm.cuh"
+#include "vec.cuh"
 
 namespace fckl {
 
@@ -119,11 +120,6 @@ struct EpiLseT {
 };
 using EpiLse = EpiLseT<true, false>;
 using EpiEntropy = EpiLseT<false, true>;
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
 
 // Swizzled position of 16-byte chunk j of this lane's row in a staging buffer.
 __device__ __forceinline__ uint4* stage_chunk(uint8_t* buf, int lane, int j) {

@@ -8,11 +8,14 @@ upstream gradient in backward.
 """
 from __future__ import annotations
 
+import dataclasses
+
 import torch
 
-from . import (FcklCeProblem, FcklError, FcklProblem, FCKL_GRAD_BFLOAT, FCKL_GRAD_FLOAT,
-               FCKL_LABELS_INT, FCKL_LABELS_LONG, FCKL_OK, FCKL_REDUCE_MEAN, FCKL_REDUCE_SUM,
-               fckl_ce_bwd, fckl_ce_fwd, fckl_ce_fwd_bwd, fckl_ce_workspace_bytes, fckl_check,
+from . import (FcklCeProblem, FcklError, FcklNormProblem, FcklProblem, FCKL_BFLOAT, FCKL_FLOAT,
+               FCKL_GRAD_BFLOAT, FCKL_GRAD_FLOAT, FCKL_LABELS_INT, FCKL_LABELS_LONG,
+               FCKL_NORM_POST, FCKL_NORM_PRE, FCKL_OK, FCKL_REDUCE_MEAN, FCKL_REDUCE_SUM,
+               fckl_block_norm_bwd, fckl_block_norm_fwd, fckl_block_norm_workspace_bytes, fckl_ce_bwd, fckl_ce_fwd, fckl_ce_fwd_bwd, fckl_ce_workspace_bytes, fckl_check,
                fckl_fwd, fckl_fwd_bwd, fckl_fwd_bwd_host, fckl_fwd_bwd_sliced,
                fckl_host_workspace_bytes, fckl_scale_gradient, fckl_workspace_bytes)
 
@@ -21,7 +24,8 @@ __all__ = ["make_problem", "alloc_workspace", "fused_kl_fwd", "fused_kl_fwd_bwd"
            "fused_kl_from_host", "alloc_host_workspace", "fused_kl_fwd_bwd_host",
            "fused_kl_fwd_bwd_sliced",
            "FusedChunkedKL", "fused_chunked_kl_loss", "fused_ce_fwd", "fused_ce_fwd_bwd",
-           "fused_ce_bwd", "FusedCrossEntropy", "fused_cross_entropy_loss"]
+           "fused_ce_bwd", "FusedCrossEntropy", "fused_cross_entropy_loss", "block_norm_fwd",
+           "block_norm_bwd", "BlockNorm", "block_norm", "TailNorm"]
 
 
 def _bits(t: torch.Tensor) -> torch.Tensor:
@@ -289,7 +293,12 @@ class FusedChunkedKL(torch.autograd.Function):
                 None, None, None, None, None)
 
 
-def fused_chunked_kl_loss(hidden, W, topk_idx, topk_logit, row_mask=None, T=1.0, chunk=0):
+def fused_chunked_kl_loss(hidden, W, topk_idx, topk_logit, row_mask=None, T=1.0, chunk=0,
+                          norm=None):
+    """``norm``: a TailNorm; ``hidden`` is then the residual stream, and the loss
+    runs over its normed rows."""
+    if norm is not None:
+        hidden = norm(hidden)
     return FusedChunkedKL.apply(hidden, W, topk_idx, topk_logit, row_mask, T, chunk)
 
 
@@ -610,15 +619,193 @@ class FusedCrossEntropy(torch.autograd.Function):
 
 
 def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0,
-                             z_loss=0.0, ignore_index=-100, reduction="mean", chunk=0, check=True):
+                             z_loss=0.0, ignore_index=-100, reduction="mean", chunk=0, check=True,
+                             norm=None):
     """Differentiable fused_ce_fwd: the loss (a scalar), or with reduction "none"
     the row losses [N].  hidden and W are bfloat16; ``row_weight`` gets no
     gradient.  ``check=False`` leaves out the device-error check, which
-    synchronises the stream."""
+    synchronises the stream.  ``norm``: a TailNorm; ``hidden`` is then the
+    residual stream, and the loss runs over its normed rows."""
     if row_weight is not None and row_weight.requires_grad:
         raise ValueError("row_weight gets no gradient; detach it")
     if reduction not in ("mean", "sum", "none"):
         raise ValueError(f'reduction must be "mean", "sum" or "none", got {reduction!r}')
+    if norm is not None:
+        hidden = norm(hidden)
     opts = dict(T=T, label_smoothing=label_smoothing, z_loss=z_loss, chunk=chunk)
     return FusedCrossEntropy.apply(hidden, W, labels, row_weight, reduction, ignore_index, check,
                                    opts)
+
+
+# ---------------------------------------------------------------- norms around a block
+_REAL_TYPES = {torch.float32: FCKL_FLOAT, torch.bfloat16: FCKL_BFLOAT}
+
+
+def _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps, weight_offset,
+                  dy=None, dv=None):
+    """Checks of a block_norm call and its problem."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N,H]; got {tuple(x.shape)}")
+    N, H = x.shape
+    rows = (("x", x), ("block", block), ("dy", dy), ("dv", dv))
+    for name, t in rows:
+        if t is not None and tuple(t.shape) != (N, H):
+            raise ValueError(f"{name} must be [N={N},H={H}]; got {tuple(t.shape)}")
+    if x.dtype not in _REAL_TYPES:
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if block is not None and block.dtype != torch.bfloat16:
+        raise TypeError(f"block must be bfloat16, got {block.dtype}")
+    if dv is not None and dv.dtype != x.dtype:
+        raise TypeError(f"dv must have x's dtype {x.dtype}, got {dv.dtype}")
+    if dy is not None and dy.dtype not in _REAL_TYPES:
+        raise TypeError(f"dy must be float32 or bfloat16, got {dy.dtype}")
+    weights = [(n, w) for n, w in (("post_weight", post_weight), ("gate", gate),
+                                   ("pre_weight", pre_weight)) if w is not None]
+    for name, w in weights:
+        if tuple(w.shape) != (H,):
+            raise ValueError(f"{name} must be [H={H}]; got {tuple(w.shape)}")
+        if w.dtype not in _REAL_TYPES or w.dtype != weights[0][1].dtype:
+            raise TypeError("post_weight, gate and pre_weight must all be float32 or all bfloat16")
+    _check_placement(True, rows + tuple(weights))
+    flags = (FCKL_NORM_POST if post else 0) | (FCKL_NORM_PRE if pre else 0)
+    wt = _REAL_TYPES[weights[0][1].dtype] if weights else FCKL_FLOAT
+    return FcklNormProblem(N, H, scale, eps, weight_offset, flags, _REAL_TYPES[x.dtype], wt,
+                           FCKL_BFLOAT if dy is None else _REAL_TYPES[dy.dtype])
+
+
+def block_norm_fwd(x, block=None, post_weight=None, gate=None, pre_weight=None, scale=1.0,
+                   post=None, pre=True, eps=1e-6, weight_offset=0.0, want_residual=True):
+    """Joins a block's output to the residual stream and norms the result:
+    v = x + scale * gate * (block * rho(block) * post_weight), y = v * rho(v) *
+    pre_weight with rho(z) = 1/sqrt(mean(z^2) + eps) over a row.
+
+    x [N,H] float32 or bfloat16, block [N,H] bfloat16 (None: a plain norm of x),
+    weights and gate [H] float32 or bfloat16 (None: ones; ``weight_offset`` is
+    added to the two norm weights).  ``post`` (default: whether post_weight is
+    given) and ``pre``: which norms there are.  Returns (v in x's dtype, y
+    bfloat16); v is x itself without a block and None without ``want_residual``;
+    y is None without ``pre``."""
+    post = post_weight is not None if post is None else bool(post)
+    prob = _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps,
+                         weight_offset)
+    dev = x.device
+    v = torch.empty_like(x) if block is not None and (want_residual or not pre) else None
+    y = torch.empty(prob.N, prob.H, dtype=torch.bfloat16, device=dev) if pre else None
+    with torch.cuda.device(dev):
+        st = fckl_block_norm_fwd(prob, x.data_ptr(), _ptr(block), _ptr(post_weight), _ptr(gate),
+                                 _ptr(pre_weight), _ptr(v), _ptr(y),
+                                 torch.cuda.current_stream(dev).cuda_stream)
+    if st != FCKL_OK:
+        raise FcklError(st, "fckl_block_norm_fwd")
+    return (x if block is None else v), y
+
+
+def block_norm_bwd(x, block=None, dy=None, dv=None, post_weight=None, gate=None, pre_weight=None,
+                   scale=1.0, post=None, pre=True, eps=1e-6, weight_offset=0.0,
+                   want=(True, True, True, True, True), workspace=None):
+    """Gradients of block_norm_fwd's inputs from dy (float32 or bfloat16, with
+    ``pre``) and dv (x's dtype, or None).  Returns (dx, dblock, dpost_weight,
+    dgate, dpre_weight), the last three float32; None for what is not there or
+    not in ``want``."""
+    post = post_weight is not None if post is None else bool(post)
+    if pre and dy is None:
+        raise ValueError("dy is required with a pre-norm")
+    if not pre and (dy is not None or dv is None):
+        raise ValueError("without a pre-norm there is dv and no dy")
+    prob = _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps,
+                         weight_offset, dy, dv)
+    dev = x.device
+    if workspace is None:
+        nbytes = fckl_block_norm_workspace_bytes(prob)
+        if nbytes == 0:
+            raise FcklError(1 if prob.H % 8 == 0 and prob.H <= 8192 else 2,
+                            "fckl_block_norm_workspace_bytes")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
+          or workspace.device != dev):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    dx = torch.empty_like(x) if want[0] else None
+    dblock = torch.empty_like(block) if want[1] and block is not None else None
+    dws = [torch.empty(prob.H, dtype=torch.float32, device=dev) if on and w is not None else None
+           for on, w in zip(want[2:], (post_weight, gate, pre_weight))]
+    if dx is None and dblock is None and not any(d is not None for d in dws):
+        return None, None, None, None, None
+    with torch.cuda.device(dev):
+        st = fckl_block_norm_bwd(prob, x.data_ptr(), _ptr(block), _ptr(post_weight), _ptr(gate),
+                                 _ptr(pre_weight), _ptr(dy), _ptr(dv), _ptr(dx), _ptr(dblock),
+                                 _ptr(dws[0]), _ptr(dws[1]), _ptr(dws[2]), workspace.data_ptr(),
+                                 workspace.numel(), torch.cuda.current_stream(dev).cuda_stream)
+    if st != FCKL_OK:
+        raise FcklError(st, "fckl_block_norm_bwd")
+    return dx, dblock, dws[0], dws[1], dws[2]
+
+
+class BlockNorm(torch.autograd.Function):
+    """(v, y), y alone (no block) or v alone (no pre-norm) of block_norm_fwd, with
+    gradients for x, block, the weights and the gate in their own dtypes."""
+
+    @staticmethod
+    def forward(ctx, x, block, post_weight, gate, pre_weight, opts):
+        ctx.set_materialize_grads(False)
+        ctx.opts = opts
+        ctx.save_for_backward(x, block, post_weight, gate, pre_weight)
+        v, y = block_norm_fwd(x, block, post_weight, gate, pre_weight, **opts)
+        ctx.single = block is None or y is None
+        return y if block is None else v if y is None else (v, y)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        x, block, post_weight, gate, pre_weight = ctx.saved_tensors
+        opts = dict(ctx.opts)
+        if not ctx.single:
+            dv, dy = grads
+        else:
+            dv, dy = (None, grads[0]) if opts["pre"] else (grads[0], None)
+        if dv is None and dy is None:
+            return (None,) * 6
+        if dy is None:              # y took no part in what is differentiated
+            opts["pre"] = False
+        want = ctx.needs_input_grad[:5]
+        if not opts["pre"]:
+            want = want[:4] + (False,)
+            pre_weight_in = None
+        else:
+            pre_weight_in = pre_weight
+        out = block_norm_bwd(x, block, None if dy is None else dy.contiguous(),
+                             None if dv is None else dv.contiguous(), post_weight, gate,
+                             pre_weight_in, want=want, **opts)
+        weights = (post_weight, gate, pre_weight)
+        return out[:2] + tuple(g if g is None else g.to(w.dtype)
+                               for g, w in zip(out[2:], weights)) + (None,)
+
+
+def block_norm(x, block=None, post_weight=None, gate=None, pre_weight=None, scale=1.0, post=None,
+               pre=True, eps=1e-6, weight_offset=0.0):
+    """Differentiable block_norm_fwd: (v, y)."""
+    if block is None and not pre:
+        raise ValueError("without a block there must be a pre-norm")
+    opts = dict(scale=scale, post=post_weight is not None if post is None else bool(post),
+                pre=bool(pre), eps=eps, weight_offset=weight_offset)
+    out = BlockNorm.apply(x, block, post_weight, gate, pre_weight, opts)
+    if block is None:
+        return x, out
+    return out if pre else (out, None)
+
+
+@dataclasses.dataclass
+class TailNorm:
+    """The end of a student between its residual stream and its projection, for
+    the losses' ``norm`` option: the last block's output (if any) joins the
+    stream and the stream is normed (see block_norm_fwd)."""
+    pre_weight: torch.Tensor = None
+    block: torch.Tensor = None
+    post_weight: torch.Tensor = None
+    gate: torch.Tensor = None
+    scale: float = 1.0
+    post: bool = None
+    eps: float = 1e-6
+    weight_offset: float = 0.0
+
+    def __call__(self, x):
+        return block_norm(x, self.block, self.post_weight, self.gate, self.pre_weight, self.scale,
+                          self.post, True, self.eps, self.weight_offset)[1]

@@ -373,6 +373,60 @@ fckl_status fckl_ce_bwd(const fckl_ce_problem* prob, const void* hidden, const v
 fckl_status fckl_scale_gradient(void* grad, int64_t n, int32_t grad_type, const float* factor,
                                 void* stream);
 
+/* ----------------------------------------------------------------------------
+ * The norms around a block, fused with its gate and residual scale (how the
+ * rows that enter the loss are made: the last block's output joins the residual
+ * stream, and the stream is normed ahead of the projection; an addition of this
+ * library).  Per row of H values:
+ *   u = block rho(block) post_weight      (FCKL_NORM_POST; else u = block)
+ *   v = x + scale gate u                  the new residual stream
+ *   y = v rho(v) pre_weight               (FCKL_NORM_PRE) what the next block, or
+ *                                         the projection, reads
+ *   rho(z) = 1 / sqrt(mean(z^2) + eps)
+ * x, v, dx, dv: [N, H] in x_type; block, y, dblock: [N, H] bf16; dy: [N, H] in
+ * dy_type; post_weight, gate, pre_weight: [H] in weight_type, NULL = ones, with
+ * weight_offset added to the two norm weights (1 for weights stored around 0);
+ * dpost_weight, dgate, dpre_weight: [H] fp32.  Sums are fp32; v is normed before
+ * it is rounded, and each output is rounded once.
+ * block = NULL is a plain norm of x (FCKL_NORM_PRE alone, no gate, v = NULL).
+ * Rows contiguous, pointers 16-byte aligned, outputs must not overlap inputs or
+ * each other; H % 8 == 0 and H <= 8192, else FCKL_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+typedef enum { FCKL_FLOAT = 0, FCKL_BFLOAT = 1 } fckl_real_type; /* fp32, bf16 */
+enum { FCKL_NORM_POST = 1, FCKL_NORM_PRE = 2 };
+
+typedef struct {
+  int64_t N;            /* rows                                   */
+  int64_t H;            /* values per row                         */
+  float scale;          /* residual scale                         */
+  float eps;            /* >= 0                                   */
+  float weight_offset;  /* added to post_weight and pre_weight    */
+  int32_t flags;        /* FCKL_NORM_POST | FCKL_NORM_PRE         */
+  int32_t x_type;       /* fckl_real_type of x, v, dx, dv         */
+  int32_t weight_type;  /* fckl_real_type of the weights and gate */
+  int32_t dy_type;      /* fckl_real_type of dy (backward)        */
+} fckl_norm_problem;
+
+/* v may be NULL when y is wanted alone; y is given exactly with FCKL_NORM_PRE. */
+fckl_status fckl_block_norm_fwd(const fckl_norm_problem* prob, const void* x, const void* block,
+                                const void* post_weight, const void* gate, const void* pre_weight,
+                                void* v, void* y, void* stream);
+
+/* Device workspace of fckl_block_norm_bwd (0 when the problem is invalid): fp32
+ * partial sums of the weight gradients. */
+size_t fckl_block_norm_workspace_bytes(const fckl_norm_problem* prob);
+
+/* Gradients for the inputs of fckl_block_norm_fwd, from dy (given exactly with
+ * FCKL_NORM_PRE) and dv (the gradient that reaches the new residual stream from
+ * elsewhere; NULL = zeros, required without FCKL_NORM_PRE).  Outputs may be NULL
+ * when not wanted; the gradient of a weight that is not given must be.
+ * Repeated calls give the same bits. */
+fckl_status fckl_block_norm_bwd(const fckl_norm_problem* prob, const void* x, const void* block,
+                                const void* post_weight, const void* gate, const void* pre_weight,
+                                const void* dy, const void* dv, void* dx, void* dblock,
+                                float* dpost_weight, float* dgate, float* dpre_weight,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then returns the first device-side error recorded in
  * `workspace` by the last call that used it (FCKL_OK if none), or
  * FCKL_ERR_CUDA if the stream reports a CUDA error. */
@@ -400,7 +454,7 @@ const char* fckl_status_string(fckl_status status);
  *        9 merge_entropy, 10 gather_rows, 11 scatter_rows (reserved: gathered
  *        rows write their results in place, no kernel of this kind runs),
  *        12 select_rows, 13 zero_dw, 14 ce_logits, 15 ce_dlogits, 16 dH_rows,
- *        17 dW_round. */
+ *        17 dW_round, 18 norm_fwd, 19 norm_bwd, 20 norm_sum. */
 typedef struct {
   char name[32];     /* kernel kind, e.g. "fwd_logits_lse" */
   int64_t launches;  /* launches recorded */

@@ -22,3 +22,4 @@ from .kl import (  # noqa: F401
 )
 from .selective import student_entropy, select_top_rows  # noqa: F401
 from .cross_entropy import cross_entropy  # noqa: F401
+from .block_norm import block_norm, block_norm_grads  # noqa: F401
