@@ -1,7 +1,10 @@
 // Host side of the vocabulary cross entropy: checks, workspace layout and the
 // chunk loop.  Per chunk of C kept rows, on the caller's stream:
-//   gather rows -> logits GEMM (log-sum-exp epilogue) -> merge (row losses)
-//   [-> recompute GEMM (dlogits epilogue) -> dH GEMM -> dW GEMM -> dH rows].
+//   gather rows -> logits GEMM (log-sum-exp epilogue) -> merge (row losses),
+// with gradients
+//   gather rows -> logits GEMM (and its exponentials) -> merge and dlogits, or,
+//   for given log-sum-exps, gather rows -> logits GEMM (dlogits epilogue),
+//   -> dH GEMM -> dW GEMM -> dH rows.
 #include <algorithm>
 #include <cmath>
 
@@ -118,7 +121,9 @@ const CeDevice* ce_device() {
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     d.ok = major == 10 && minor == 0 && d.sms > 1 && allow_smem<EpiCe<false>, false, false>() &&
-           allow_smem<EpiCe<true>, false, false>() && allow_smem<EpiCeDlogits, false, false>() &&
+           allow_smem<EpiCe<true>, false, false>() &&
+           allow_smem<EpiCeStore<false>, false, false>() &&
+           allow_smem<EpiCeStore<true>, false, false>() && allow_smem<EpiCeDlogits, false, false>() &&
            allow_smem<EpiCeDH, false, true>() && allow_smem<EpiCeDW, true, true>() &&
            allow_smem<EpiCeDWSum, true, true>();
   }
@@ -216,40 +221,53 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     if (!make_map(&mapH_k, hst, H, cap, (long long)H * 2, BK, CM)) return FCKL_ERR_CUDA;
     SchedArgs sa_v{SCHED_VOCAB_MAJOR, NT, KBh, 1, 0, rc, 0, 0};
     const int Gv = grid_for(MT * NT);
-    if (losses) {
+    CUtensorMap mapD_st, mapD_k, mapD_mn, mapH_mn;
+    if (grads && !make_map(&mapD_st, dlog, L.Vp, cap, L.Vp * 2, 64, 32)) return FCKL_ERR_CUDA;
+    const float* zs = smooth ? zsum : nullptr;
+    // The GEMM over h W^T: its row count, hence its work, is read on the device.
+#define FCKL_CE_GEMM(Epi, map, params)                                                       \
+  FCKL_LAUNCH((gemm_pair_kernel<Epi, false, false>), Gv, GEMM_THREADS, pair_smem_bytes<Epi>(), \
+              mapH_k, mapW_k, map, params, sa_v, ca)
+    if (q.mode == CeMode::kFwd) {
       {
         ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + nr * NT * 8.0);
         if (smooth) {
           EpiCe<true>::Params pf{V, NT, scale2, lab, zlab, part, zsum};
-          FCKL_LAUNCH((gemm_pair_kernel<EpiCe<true>, false, false>), Gv, GEMM_THREADS,
-                      pair_smem_bytes<EpiCe<true>>(), mapH_k, mapW_k, mapW_k, pf, sa_v, ca);
+          FCKL_CE_GEMM(EpiCe<true>, mapW_k, pf);
         } else {
           EpiCe<false>::Params pf{V, NT, scale2, lab, zlab, part, nullptr};
-          FCKL_LAUNCH((gemm_pair_kernel<EpiCe<false>, false, false>), Gv, GEMM_THREADS,
-                      pair_smem_bytes<EpiCe<false>>(), mapH_k, mapW_k, mapW_k, pf, sa_v, ca);
+          FCKL_CE_GEMM(EpiCe<false>, mapW_k, pf);
         }
       }
       ProfScope ps(K_MERGE, st, 0.0, nr * (NT * 8.0 + 28.0));
-      FCKL_LAUNCH(k_ce_merge, (int)cdiv(cap, kCeWarps), kCeWarps * 32, 0, (const float2*)part,
-                  (const float*)(smooth ? zsum : nullptr), NT, rc, cap, V, invT,
-                  prob->label_smoothing, prob->z_loss, clist, (const float*)zlab, (const float*)kw,
-                  lse2, q.row_loss, q.lse_out, share + row0);
+      FCKL_LAUNCH(k_ce_merge, (int)cdiv(cap, kCeWarps), kCeWarps * 32, 0, (const float2*)part, zs,
+                  NT, rc, cap, V, invT, prob->label_smoothing, prob->z_loss, clist,
+                  (const float*)zlab, (const float*)kw, q.row_loss, q.lse_out, share + row0);
+      continue;
     }
-    if (!grads) continue;
-
-    // The recompute GEMM's operands (the gathered rows, W) were complete before
-    // the merge launched; without a merge it follows the gather directly.
-    SchedArgs sa_b = sa_v;
-    sa_b.early = losses ? 1 : 0;
-    CUtensorMap mapD_st, mapD_k, mapD_mn, mapH_mn;
-    if (!make_map(&mapD_st, dlog, L.Vp, cap, L.Vp * 2, 64, 32)) return FCKL_ERR_CUDA;
-    {
+    if (q.mode == CeMode::kFwdBwd) {
+      {
+        ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
+        if (smooth) {
+          EpiCeStore<true>::Params pf{V, NT, scale2, lab, zlab, part, zsum, cap};
+          FCKL_CE_GEMM(EpiCeStore<true>, mapD_st, pf);
+        } else {
+          EpiCeStore<false>::Params pf{V, NT, scale2, lab, zlab, part, nullptr, cap};
+          FCKL_CE_GEMM(EpiCeStore<false>, mapD_st, pf);
+        }
+      }
+      ProfScope ps(K_CE_SCALE, st, 0.0, nr * (V * 4.0 + NT * 16.0));
+      FCKL_LAUNCH(k_ce_dlogits, cap, 256, 0, (const float2*)part, zs, NT, rc, V, L.Vp, invT,
+                  prob->label_smoothing, prob->z_loss, clist, (const int*)lab, (const float*)zlab,
+                  (const float*)kw, reinterpret_cast<uint4*>(dlog), q.row_loss, q.lse_out,
+                  share + row0);
+    } else {
       EpiCeDlogits::Params pb{V, scale2, prob->label_smoothing, 2.f * prob->z_loss, lab, kw, lse2,
                               cap};
       ProfScope ps(K_CE_DLOGITS, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
-      FCKL_LAUNCH((gemm_pair_kernel<EpiCeDlogits, false, false>), Gv, GEMM_THREADS,
-                  pair_smem_bytes<EpiCeDlogits>(), mapH_k, mapW_k, mapD_st, pb, sa_b, ca);
+      FCKL_CE_GEMM(EpiCeDlogits, mapD_st, pb);
     }
+#undef FCKL_CE_GEMM
     if (q.dH) {
       if (!make_map(&mapD_k, dlog, V, cap, L.Vp * 2, BK, CM)) return FCKL_ERR_CUDA;
       SchedArgs sa_h{SCHED_SPLIT_K, NTh, KBv, 0, 0, rc, 0, w3d, 0, narrow_h, 0, 2, 1,

@@ -13,6 +13,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "epilogues.cuh"
 #include "gemm.cuh"
@@ -214,7 +215,127 @@ struct EpiCe {
   static __device__ void finish(const Params&, State&, int) {}
 };
 
-// Backward: recomputed z tile -> G (see the top), rounded once to bf16 and
+// Forward of a call that also wants gradients: as EpiCe, and the exponentials
+// themselves are kept, E = 2^(a2 - m) per tile with m = (the row's tile maximum)
+// - 15, as fp16 in the chunk's [rows, Vp] block; k_ce_dlogits turns them into
+// dlogits in place once the row's LSE is known.  So the backward needs no second
+// logits product (6 H V flops per row instead of 8, for 4 V more bytes: at
+// H = 4096 the product costs about 10 times what the bytes do).
+// fp16 because E is rounded here and G once more in k_ce_dlogits: 2^-11 against
+// G's own 2^-8; in bf16 the two roundings would add up.  With the offset of 15
+// the tile's largest E is 2^15 and E stays normal down to 2^-29 of it.
+// The accumulator is read twice (maximum, then exponentials).
+template <bool kSum>
+struct EpiCeStore {
+  static constexpr uint32_t kSmemBytes = 4 * 2 * 4096;
+  static constexpr bool kUsesMapC = true;  // map C: [rows, Vp] 16-bit, box {64, 32}
+  struct Params {
+    int V, NT;
+    float scale2;
+    const int* lab;
+    float* zlab;
+    float2* partials;      // [rows, NT] (m, sum of E before rounding)
+    float* zsum;
+    int store_rows;
+  };
+  struct State {
+    int n;
+    uint8_t* buf;
+  };
+  static __device__ void init(const Params&, State& st, uint8_t* smem_warp, int) {
+    st.n = 0; st.buf = smem_warp;
+  }
+  static __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ void exps(float (&v)[32], float scale2, float ref, int cols,
+                                              float& sum) {
+    if (cols >= 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = ex2_approx(fmaf(v[j], scale2, -ref));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = j < cols ? ex2_approx(fmaf(v[j], scale2, -ref)) : 0.f;
+    }
+    float acc = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc += v[j];
+    sum += acc;
+  }
+  static __device__ void tile(const Params& p, State& st, const Work& w, uint32_t taddr, int r,
+                              const CUtensorMap* mapC, int quarter, int lane) {
+    const int row = w.m0 + r;
+    const bool rv = row < w.rows;
+    const int y = rv ? __ldg(p.lab + row) - w.n0 : -1;
+    float top = -INFINITY, u = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < BN / 32; ++c) {
+      float v[32];
+      tmem_ld32_conv(taddr + (uint32_t)(c * 32), v);
+      const int cols = rv ? p.V - (w.n0 + c * 32) : 0;
+      if ((y >> 5) == c) {
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z = (j == (y & 31)) ? v[j] : z;
+        p.zlab[row] = z;
+      }
+      if (kSum) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) u += j < cols ? v[j] : 0.f;
+      }
+      if (cols >= 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) top = j < cols ? fmaxf(top, v[j]) : top;
+      }
+    }
+    const float m = fmaf(top, p.scale2, -15.f);
+    const float ref = m == -INFINITY ? 0.f : m;  // a tile of -inf only adds 0, not NaN
+    float s = 0.f;
+    const int y0 = w.m0 + quarter * 32;
+    const int y_end = min((w.rows + 63) & ~63, p.store_rows);
+#pragma unroll 1
+    for (int c = 0; c < BN / 64; ++c) {
+      const int base = w.n0 + c * 64;
+      const int cols = rv ? p.V - base : 0;
+      float v0[32], v1[32];
+      tmem_ld32_conv(taddr + (uint32_t)(c * 64), v0);
+      tmem_ld32_conv(taddr + (uint32_t)(c * 64 + 32), v1);
+      exps(v0, p.scale2, ref, cols, s);
+      exps(v1, p.scale2, ref, cols - 32, s);
+      uint8_t* buf = st.buf + (st.n & 1) * 4096;
+      stage_acquire(lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        *stage_chunk(buf, lane, j) = make_uint4(
+            pack_half2(v0[8 * j], v0[8 * j + 1]), pack_half2(v0[8 * j + 2], v0[8 * j + 3]),
+            pack_half2(v0[8 * j + 4], v0[8 * j + 5]), pack_half2(v0[8 * j + 6], v0[8 * j + 7]));
+        *stage_chunk(buf, lane, 4 + j) = make_uint4(
+            pack_half2(v1[8 * j], v1[8 * j + 1]), pack_half2(v1[8 * j + 2], v1[8 * j + 3]),
+            pack_half2(v1[8 * j + 4], v1[8 * j + 5]), pack_half2(v1[8 * j + 6], v1[8 * j + 7]));
+      }
+      stage_release();
+      if (lane == 0) {
+        if (base < p.V && y0 < y_end) tma_store_2d(mapC, smem_u32(buf), base, y0);
+        bulk_commit();
+      }
+      ++st.n;
+    }
+    if (rv) {
+      p.partials[(size_t)row * p.NT + w.nt] = make_float2(m, s);
+      if (kSum) p.zsum[(size_t)row * p.NT + w.nt] = u;
+    }
+  }
+  static __device__ void finish(const Params&, State&, int lane) {
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+};
+
+// Backward without the forward's exponentials (the row-gradient call): recomputed z tile -> G (see the top), rounded once to bf16 and
 // TMA-stored to the chunk's [rows, Vp] block.  Columns in [V, Vp) and the rows
 // behind the last one, up to the next multiple of 64, are stored as zeros.
 struct EpiCeDlogits {
@@ -390,18 +511,18 @@ struct EpiCeDW {
 };
 
 // ---------------------------------------------------------------- row kernels
-// Merges the tile partials of each row into its LSE and row loss.  Kept rows
-// write lse2[i] for the recompute GEMM, and all rows of the chunk's part of
-// the list write the caller's row loss and LSE (0 for left-out rows) and their
-// share k_r l_r of the loss (list order).  One warp per row.
+// Merges the tile partials of each row into its LSE and row loss.  All rows of
+// the chunk's part of the list write the caller's row loss and LSE (0 for
+// left-out rows) and their share k_r l_r of the loss (list order).  One warp
+// per row.
 __global__ void __launch_bounds__(kCeWarps * 32)
     k_ce_merge(const float2* __restrict__ partials, const float* __restrict__ zsum, int NT,
                RowCount rc, int cap, int V, float invT, float smooth, float zloss,
                const int32_t* __restrict__ list, const float* __restrict__ zlab,
-               const float* __restrict__ kw, float* __restrict__ lse2, float* __restrict__ row_loss,
+               const float* __restrict__ kw, float* __restrict__ row_loss,
                float* __restrict__ lse_out, float* __restrict__ share) {
-  pdl_trigger();  // the recompute GEMM after it may start its main loop
   pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kCeWarps + (threadIdx.x >> 5);
   if (row >= cap) return;
@@ -433,10 +554,101 @@ __global__ void __launch_bounds__(kCeWarps * 32)
     float l = nll;
     if (smooth > 0.f) l += smooth * ((lse - Z / (float)V * invT) - nll);
     l = fmaf(zloss * lse, lse, l);
-    lse2[row] = L2;
     if (row_loss) row_loss[r] = l;
     if (lse_out) lse_out[r] = lse;
     share[row] = kw[row] * l;
+  }
+}
+
+// Merge of EpiCeStore's partials, as k_ce_merge, and the row's dlogits from the
+// stored exponentials, in place: fp16 E -> bf16 G = kap E 2^(m_t - L2) - targets,
+// rounded once.  The label's entry is formed from its fp32 logit: q_y - 1 would
+// lose what E's rounding cuts off where the row is confident.  One block per
+// row: 8 warps, a warp at a time on a tile of 256 columns (16 bytes a lane).
+// Bound by HBM: 4 bytes per entry.
+__global__ void __launch_bounds__(256)
+    k_ce_dlogits(const float2* __restrict__ partials, const float* __restrict__ zsum, int NT,
+                 RowCount rc, int V, long long Vp, float invT, float smooth, float zloss,
+                 const int32_t* __restrict__ list, const int* __restrict__ lab,
+                 const float* __restrict__ zlab, const float* __restrict__ kw,
+                 uint4* __restrict__ dlog, float* __restrict__ row_loss,
+                 float* __restrict__ lse_out, float* __restrict__ share) {
+  __shared__ float red[3][8];
+  pdl_wait();
+  pdl_trigger();
+  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = list[row];
+  if (row >= rc.get()) {
+    if (threadIdx.x == 0) {
+      if (row_loss) row_loss[r] = 0.f;
+      if (lse_out) lse_out[r] = 0.f;
+      share[row] = 0.f;
+    }
+    return;
+  }
+  const float2* pr = partials + (size_t)row * NT;
+  float M = -INFINITY, S = 0.f, Z = 0.f;
+  for (int t = threadIdx.x; t < NT; t += 256) {
+    const float2 q = pr[t];
+    const float nm = fmaxf(M, q.x);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    S = S * exp2f(M - ref) + q.y * exp2f(q.x - ref);
+    M = nm;
+    if (zsum) Z += zsum[(size_t)row * NT + t];
+  }
+  const float Mw = warp_max(M);
+  S = warp_sum(S * exp2f(M - (Mw == -INFINITY ? 0.f : Mw)));
+  if (zsum) Z = warp_sum(Z);
+  if (lane == 0) { red[0][warp] = Mw; red[1][warp] = S; red[2][warp] = Z; }
+  __syncthreads();
+  M = red[0][0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) M = fmaxf(M, red[0][k]);
+  S = Z = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    S += red[1][k] * exp2f(red[0][k] - (M == -INFINITY ? 0.f : M));
+    Z += red[2][k];
+  }
+  const float L2 = M + log2f(S), lse = L2 * kLn2, k0 = kw[row], a_y = zlab[row] * invT;
+  if (threadIdx.x == 0) {
+    const float nll = lse - a_y;
+    float l = nll;
+    if (smooth > 0.f) l += smooth * ((lse - Z / (float)V * invT) - nll);
+    l = fmaf(zloss * lse, lse, l);
+    if (row_loss) row_loss[r] = l;
+    if (lse_out) lse_out[r] = lse;
+    share[row] = k0 * l;
+  }
+  const float kap = k0 * fmaf(2.f * zloss, lse, 1.f);
+  const float label_mass = k0 * (1.f - smooth), base_mass = k0 * smooth / (float)V;
+  const int y = lab[row];
+  const float g_y = fmaf(kap, exp2f(fmaf(zlab[row], invT * kLog2e, -L2)), -(label_mass + base_mass));
+  uint4* dr = dlog + (size_t)row * (Vp / 8);
+#pragma unroll 4
+  for (int t = warp; t < NT; t += 8) {
+    const int col = t * BN + lane * 8;
+    if (col >= Vp) continue;
+    const float f = kap * ex2_approx(pr[t].x - L2);
+    uint4 q = dr[col / 8];
+    float v[8];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      v[2 * j] = fmaf(f, e.x, -base_mass);
+      v[2 * j + 1] = fmaf(f, e.y, -base_mass);
+    }
+    if ((unsigned)(y - col) < 8u) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j == y - col ? g_y : v[j];
+    }
+    if (col + 8 > V) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = col + j < V ? v[j] : 0.f;
+    }
+    dr[col / 8] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
 }
 

@@ -354,7 +354,9 @@ fckl_status fckl_ce_fwd(const fckl_ce_problem* prob, const void* hidden, const v
 
 /* Forward and backward in one call: dH [N, H] and dW [V, H] of `loss`, in
  * grad_type, overwritten.  row_loss and lse may be NULL, and so may one of dH
- * and dW (a frozen projection, or frozen rows: that product is not computed). */
+ * and dW (a frozen projection, or frozen rows: that product is not computed).
+ * 6*H*V flops per kept row: the forward keeps one chunk's exponentials in the
+ * block that dlogits then takes, so nothing is computed twice. */
 fckl_status fckl_ce_fwd_bwd(const fckl_ce_problem* prob, const void* hidden, const void* W,
                             const void* labels, const float* row_weight, float* loss,
                             float* row_loss, float* lse, void* dH, void* dW, void* workspace,
@@ -454,7 +456,8 @@ const char* fckl_status_string(fckl_status status);
  *        9 merge_entropy, 10 gather_rows, 11 scatter_rows (reserved: gathered
  *        rows write their results in place, no kernel of this kind runs),
  *        12 select_rows, 13 zero_dw, 14 ce_logits, 15 ce_dlogits, 16 dH_rows,
- *        17 dW_round, 18 norm_fwd, 19 norm_bwd, 20 norm_sum. */
+ *        17 dW_round, 18 norm_fwd, 19 norm_bwd, 20 norm_sum,
+ *        21 ce_scale. */
 typedef struct {
   char name[32];     /* kernel kind, e.g. "fwd_logits_lse" */
   int64_t launches;  /* launches recorded */

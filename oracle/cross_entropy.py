@@ -23,8 +23,10 @@ def cross_entropy(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0
                   ignore_index=-100, reduction="mean", row_grad=None):
     """Dict with loss, row_loss [N], lse [N], dH [N, H], dW [V, H], and the
     magnitudes |G| |W| / T and |G|^T |h| / T (dH_abs, dW_abs) that bound what a
-    relative rounding of G's entries can change.  ``row_grad`` replaces the
-    rows' factors w_r / D in the gradients."""
+    relative rounding of G's entries can change, and the same with the positive
+    part k q (1 + 2 lam LSE) in G's place (dH_q, dW_q), for relative errors of
+    q ahead of the subtraction.  ``row_grad`` replaces the rows' factors w_r / D
+    in the gradients."""
     h = widen_bf16(hidden) if np.asarray(hidden).dtype == np.uint16 else np.asarray(hidden, np.float64)
     W = widen_bf16(W) if np.asarray(W).dtype == np.uint16 else np.asarray(W, np.float64)
     labels = np.asarray(labels, np.int64)
@@ -34,7 +36,9 @@ def cross_entropy(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0
     row_loss, lse = np.zeros(N), np.zeros(N)
     dH, dH_abs = np.zeros(h.shape), np.zeros(h.shape)
     dW, dW_abs = np.zeros(W.shape), np.zeros(W.shape)
-    out = dict(loss=0.0, row_loss=row_loss, lse=lse, dH=dH, dW=dW, dH_abs=dH_abs, dW_abs=dW_abs)
+    dH_q, dW_q = np.zeros(h.shape), np.zeros(W.shape)
+    out = dict(loss=0.0, row_loss=row_loss, lse=lse, dH=dH, dW=dW, dH_abs=dH_abs, dW_abs=dW_abs,
+               dH_q=dH_q, dW_q=dW_q)
     if keep.size == 0:
         return out
     D = float(keep.size) if reduction == "mean" else 1.0
@@ -47,11 +51,15 @@ def cross_entropy(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0
                       + z_loss * lse[keep] ** 2)
     out["loss"] = float((w[keep] * row_loss[keep]).sum() / D)
     k = (w / D if row_grad is None else np.asarray(row_grad, np.float64))[keep][:, None]
-    G = np.exp(logq) * (1 + 2 * z_loss * lse[keep])[:, None] - label_smoothing / V
+    Q = np.exp(logq) * (1 + 2 * z_loss * lse[keep])[:, None]
+    G = Q - label_smoothing / V
     G[at] -= 1 - label_smoothing
     G *= k / T
     dH[keep] = G @ W
     dW += G.T @ hk
     dH_abs[keep] = np.abs(G) @ np.abs(W)
     dW_abs += np.abs(G).T @ np.abs(hk)
+    Q = np.abs(Q * (k / T))
+    dH_q[keep] = Q @ np.abs(W)
+    dW_q += Q.T @ np.abs(hk)
     return out
