@@ -10,9 +10,6 @@ using namespace fckl;
 
 namespace {
 
-// Blocks whose weight-gradient partials the workspace has room for.
-constexpr int kNormBlocks = 4 * 148;
-
 bool valid_norm(const fckl_norm_problem* p) {
   if (p == nullptr) return false;
   if (p->N < 1 || p->H < 1 || p->N > INT32_MAX || p->H > INT32_MAX) return false;
@@ -24,8 +21,6 @@ bool valid_norm(const fckl_norm_problem* p) {
   return true;
 }
 bool supported_norm(const fckl_norm_problem* p) { return p->H % 8 == 0 && p->H <= kNormHMax; }
-
-int norm_blocks(const fckl_norm_problem* p) { return (int)std::min<long long>(p->N, kNormBlocks); }
 
 // SMs of the current device if it is an sm_100, else 0.
 int norm_sms() {
@@ -44,14 +39,41 @@ int norm_sms() {
   return known[dev] > 0 ? known[dev] : 0;
 }
 
-// Threads per block and vectors of eight values per thread.
+constexpr int kSms = 148;             // of a B200: the workspace rule needs no GPU
+constexpr size_t kRingBytes = 216 << 10;  // shared memory of an SM for the rings
+
+// Launch shape.  A row takes a warp up to 512 values, else a block of as many
+// threads as it has vectors (two vectors a thread beyond 2048 values).  `per_sm`
+// blocks share an SM: 512 threads in the backward (at up to 128 registers), 1024
+// in the forward; each gets its part of the ring memory, in 2 to 4 stages.
 struct Shape {
-  int threads, nv;
+  bool warp_row;
+  int threads, nv, per_sm, rows_per_block;
 };
-Shape norm_shape(long long H) {
+Shape norm_shape(long long H, bool bwd) {
+  Shape s{};
   const int nvec = (int)(H / 8);
-  const int nv = nvec <= 256 ? 1 : 2;
-  return Shape{(int)align_up((size_t)cdiv(nvec, nv), 32), nv};
+  s.warp_row = H <= kNormWarpH;
+  if (s.warp_row) {
+    s.nv = nvec <= 32 ? 1 : 2;
+    s.threads = kNormRowWarps * 32;
+    s.rows_per_block = kNormRowWarps;
+  } else {
+    s.nv = nvec <= 256 ? 1 : 2;
+    s.threads = (int)align_up((size_t)cdiv(nvec, s.nv), 32);
+    s.rows_per_block = 1;
+  }
+  s.per_sm = std::max(1, (bwd ? 512 : 1024) / s.threads);
+  return s;
+}
+int norm_grid(const Shape& s, long long N, int sms) {
+  return (int)std::min<long long>(cdiv(N, s.rows_per_block), (long long)sms * s.per_sm);
+}
+// Stages that fit, and the block's dynamic shared memory (`least`: bytes the
+// kernel needs there in any case).
+int norm_stages(const Shape& s, size_t row_bytes) {
+  const size_t fit = kRingBytes / s.per_sm / (row_bytes * s.rows_per_block);
+  return (int)std::max<size_t>(2, std::min<size_t>(kNormStagesMax, fit));
 }
 
 // The parts of the operation that the given arguments make impossible.
@@ -80,17 +102,43 @@ NormArgs norm_args(const fckl_norm_problem* p, const void* x, const void* block,
 using KernelFn = void (*)(const NormArgs);
 
 template <class XT, class WT>
-KernelFn pick_fwd(int nv) { return nv == 1 ? k_norm_fwd<XT, WT, 1> : k_norm_fwd<XT, WT, 2>; }
+KernelFn pick_fwd(const Shape& s) {
+  if (s.warp_row) return s.nv == 1 ? k_norm_fwd<true, XT, WT, 1> : k_norm_fwd<true, XT, WT, 2>;
+  return s.nv == 1 ? k_norm_fwd<false, XT, WT, 1> : k_norm_fwd<false, XT, WT, 2>;
+}
 template <class XT, class DT, class WT>
-KernelFn pick_bwd3(int nv) { return nv == 1 ? k_norm_bwd<XT, DT, WT, 1> : k_norm_bwd<XT, DT, WT, 2>; }
+KernelFn pick_bwd3(const Shape& s) {
+  if (s.warp_row)
+    return s.nv == 1 ? k_norm_bwd<true, XT, DT, WT, 1, 256> : k_norm_bwd<true, XT, DT, WT, 2, 256>;
+  if (s.nv == 1) return k_norm_bwd<false, XT, DT, WT, 1, 256>;
+  return s.threads <= 256 ? k_norm_bwd<false, XT, DT, WT, 2, 256>
+                          : k_norm_bwd<false, XT, DT, WT, 2, 512>;
+}
 template <class XT, class DT>
-KernelFn pick_bwd2(const fckl_norm_problem* p, int nv) {
-  return p->weight_type == FCKL_BFLOAT ? pick_bwd3<XT, DT, __nv_bfloat16>(nv)
-                                       : pick_bwd3<XT, DT, float>(nv);
+KernelFn pick_bwd2(const fckl_norm_problem* p, const Shape& s) {
+  return p->weight_type == FCKL_BFLOAT ? pick_bwd3<XT, DT, __nv_bfloat16>(s)
+                                       : pick_bwd3<XT, DT, float>(s);
 }
 template <class XT>
-KernelFn pick_bwd1(const fckl_norm_problem* p, int nv) {
-  return p->dy_type == FCKL_BFLOAT ? pick_bwd2<XT, __nv_bfloat16>(p, nv) : pick_bwd2<XT, float>(p, nv);
+KernelFn pick_bwd1(const fckl_norm_problem* p, const Shape& s) {
+  return p->dy_type == FCKL_BFLOAT ? pick_bwd2<XT, __nv_bfloat16>(p, s) : pick_bwd2<XT, float>(p, s);
+}
+
+// Dynamic shared memory beyond 48 KB has to be allowed once per kernel and
+// device.
+bool allow_smem(KernelFn k) {
+  static std::mutex mu;
+  static std::vector<std::pair<KernelFn, int>> done;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lk(mu);
+  for (const auto& d : done)
+    if (d.first == k && d.second == dev) return true;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)(SMEM_LIMIT - 1024)) != cudaSuccess)
+    return false;
+  done.emplace_back(k, dev);
+  return true;
 }
 
 }  // namespace
@@ -99,7 +147,8 @@ extern "C" {
 
 size_t fckl_block_norm_workspace_bytes(const fckl_norm_problem* prob) {
   if (!valid_norm(prob) || !supported_norm(prob)) return 0;
-  return align_up((size_t)norm_blocks(prob) * 3 * prob->H * 4, kAlign);
+  const Shape s = norm_shape(prob->H, true);
+  return align_up((size_t)norm_grid(s, prob->N, kSms) * 2 * prob->H * 4, kAlign);
 }
 
 fckl_status fckl_block_norm_fwd(const fckl_norm_problem* prob, const void* x, const void* block,
@@ -115,19 +164,21 @@ fckl_status fckl_block_norm_fwd(const fckl_norm_problem* prob, const void* x, co
   if (sms == 0) return FCKL_ERR_UNSUPPORTED;
   NormArgs a = norm_args(prob, x, block, post_weight, gate, pre_weight);
   a.v = v; a.y = y;
-  const Shape s = norm_shape(prob->H);
+  const Shape s = norm_shape(prob->H, false);
   const bool xb = prob->x_type == FCKL_BFLOAT, wb = prob->weight_type == FCKL_BFLOAT;
-  const KernelFn k = xb ? (wb ? pick_fwd<__nv_bfloat16, __nv_bfloat16>(s.nv)
-                              : pick_fwd<__nv_bfloat16, float>(s.nv))
-                        : (wb ? pick_fwd<float, __nv_bfloat16>(s.nv) : pick_fwd<float, float>(s.nv));
-  const int per_sm = std::max(1, std::min(16, 1536 / s.threads));
-  const int grid = (int)std::min<long long>(prob->N, (long long)sms * per_sm);
+  const KernelFn k = xb ? (wb ? pick_fwd<__nv_bfloat16, __nv_bfloat16>(s)
+                              : pick_fwd<__nv_bfloat16, float>(s))
+                        : (wb ? pick_fwd<float, __nv_bfloat16>(s) : pick_fwd<float, float>(s));
+  if (!allow_smem(k)) return FCKL_ERR_CUDA;
+  const int grid = norm_grid(s, prob->N, sms);
+  const size_t row_bytes = (size_t)prob->H * ((xb ? 2 : 4) + (block ? 2 : 0));
+  a.stages = norm_stages(s, row_bytes);
   const bool pdl = pdl_enabled();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const double xs = xb ? 2.0 : 4.0, n = (double)prob->N * prob->H;
   ProfScope ps(K_NORM_FWD, st, 10.0 * n,
                n * (xs + (block ? 2.0 : 0.0) + (v ? xs : 0.0) + (y ? 2.0 : 0.0)));
-  FCKL_LAUNCH(k, grid, s.threads, 0, a);
+  FCKL_LAUNCH(k, grid, s.threads, a.stages * row_bytes * s.rows_per_block, a);
   return FCKL_OK;
 }
 
@@ -156,13 +207,18 @@ fckl_status fckl_block_norm_bwd(const fckl_norm_problem* prob, const void* x, co
   NormArgs a = norm_args(prob, x, block, post_weight, gate, pre_weight);
   a.dy = dy; a.dv = dv; a.dx = dx; a.db = dblock;
   a.part = static_cast<float*>(workspace);
-  a.want_w1 = dpost_weight != nullptr;
-  a.want_g = dgate != nullptr;
-  a.want_w2 = dpre_weight != nullptr;
-  const Shape s = norm_shape(prob->H);
+  a.dw1 = dpost_weight; a.dg = dgate; a.dw2 = dpre_weight;
+  const Shape s = norm_shape(prob->H, true);
   const bool xb = prob->x_type == FCKL_BFLOAT;
-  const KernelFn k = xb ? pick_bwd1<__nv_bfloat16>(prob, s.nv) : pick_bwd1<float>(prob, s.nv);
-  const int grid = norm_blocks(prob);
+  const KernelFn k = xb ? pick_bwd1<__nv_bfloat16>(prob, s) : pick_bwd1<float>(prob, s);
+  if (!allow_smem(k)) return FCKL_ERR_CUDA;
+  const int grid = norm_grid(s, prob->N, std::min(sms, kSms));  // the workspace's partials
+  const size_t row_bytes = (size_t)prob->H * ((xb ? 2 : 4) * (dv ? 2 : 1) + (block ? 2 : 0) +
+                                              (dy ? (prob->dy_type == FCKL_BFLOAT ? 2 : 4) : 0));
+  a.stages = norm_stages(s, row_bytes);
+  size_t smem = a.stages * row_bytes * s.rows_per_block;
+  if (s.warp_row)  // the sums of the block's warps take its place at the end
+    smem = std::max(smem, (size_t)kNormRowWarps * 2 * prob->H * 4);
   const bool pdl = pdl_enabled();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const double xs = xb ? 2.0 : 4.0, n = (double)prob->N * prob->H;
@@ -170,21 +226,23 @@ fckl_status fckl_block_norm_bwd(const fckl_norm_problem* prob, const void* x, co
     ProfScope ps(K_NORM_BWD, st, 30.0 * n,
                  n * (xs + (block ? 2.0 : 0.0) + (dy ? (prob->dy_type == FCKL_BFLOAT ? 2.0 : 4.0) : 0.0) +
                       (dv ? xs : 0.0) + (dx ? xs : 0.0) + (dblock ? 2.0 : 0.0)));
-    FCKL_LAUNCH(k, grid, s.threads, 0, a);
+    FCKL_LAUNCH(k, grid, s.threads, smem, a);
   }
   if (dpost_weight || dgate || dpre_weight) {
-    ProfScope ps(K_NORM_SUM, st, 0.0, 12.0 * grid * prob->H);
+    ProfScope ps(K_NORM_SUM, st, 0.0, 8.0 * grid * prob->H);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)cdiv(prob->H, 128), 3, 1);
-    cfg.blockDim = dim3(256, 1, 1);
+    cfg.gridDim = dim3((unsigned)cdiv(prob->H, 64), 2, 1);
+    cfg.blockDim = dim3(512, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, k_norm_sum, (const float*)a.part, grid, (int)prob->H, dpost_weight,
-                           dgate, dpre_weight) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg,
+                           prob->weight_type == FCKL_BFLOAT ? k_norm_sum<__nv_bfloat16>
+                                                            : k_norm_sum<float>,
+                           (const NormArgs)a, grid) != cudaSuccess)
       return FCKL_ERR_CUDA;
   }
   return FCKL_OK;

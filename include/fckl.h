@@ -334,7 +334,9 @@ typedef struct {
   float z_loss;          /* lam >= 0                                          */
   int32_t reduction;     /* fckl_reduction                                    */
   int64_t ignore_index;  /* label of rows that do not count                   */
-  int64_t chunk;         /* rows per chunk, 0 = automatic (as fckl_problem)   */
+  int64_t chunk;         /* rows per chunk, 0 = automatic: about as many as
+                            fckl_problem's automatic chunk, at least 4096,
+                            spread evenly                                     */
   int64_t n_valid_total; /* mean: > 0 replaces the number of kept rows as D   */
   int32_t label_type;    /* fckl_label_type of labels                         */
   int32_t grad_type;     /* fckl_grad_type of dH and dW                       */

@@ -135,7 +135,8 @@ def test_workspace_rules():
     many = dict(one, N=40960)
     fp32 = fk.fckl_ce_workspace_bytes(FcklCeProblem(**many), True)
     bf16 = fk.fckl_ce_workspace_bytes(FcklCeProblem(**many, grad_type=fk.FCKL_GRAD_BFLOAT), True)
-    assert fp32 - b == 36864 * 8                 # the row list and the rows' loss shares
+    # ten chunks of 4096 rows: the row list and the rows' loss shares grow
+    assert fp32 - b == 36864 * 8
     assert bf16 - fp32 == 128256 * 1024 * 4
     small = fk.fckl_ce_workspace_bytes(FcklCeProblem(**many, chunk=256), True)
     assert small < fp32 - 3800 * 128256 * 2
