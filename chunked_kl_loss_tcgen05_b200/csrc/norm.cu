@@ -43,12 +43,13 @@ constexpr int kSms = 148;             // of a B200: the workspace rule needs no 
 constexpr size_t kRingBytes = 216 << 10;  // shared memory of an SM for the rings
 
 // Launch shape.  A row takes a warp up to 512 values, else a block of as many
-// threads as it has vectors (two vectors a thread beyond 2048 values).  `per_sm`
+// threads as it has vectors (two vectors a thread beyond 4096 values).  `per_sm`
 // blocks share an SM: 512 threads in the backward (at up to 128 registers), 1024
 // in the forward; each gets its part of the ring memory, in 2 to 4 stages.
 struct Shape {
   bool warp_row;
   int threads, nv, per_sm, rows_per_block;
+  int padded;  // values of a row in the ring (whole threads)
 };
 Shape norm_shape(long long H, bool bwd) {
   Shape s{};
@@ -59,18 +60,18 @@ Shape norm_shape(long long H, bool bwd) {
     s.threads = kNormRowWarps * 32;
     s.rows_per_block = kNormRowWarps;
   } else {
-    s.nv = nvec <= 256 ? 1 : 2;
+    s.nv = nvec <= 512 ? 1 : 2;
     s.threads = (int)align_up((size_t)cdiv(nvec, s.nv), 32);
     s.rows_per_block = 1;
   }
-  s.per_sm = std::max(1, (bwd ? 512 : 1024) / s.threads);
+  s.padded = (s.warp_row ? 32 : s.threads) * s.nv * 8;
+  s.per_sm = std::max(1, (bwd || (s.nv == 2 && !s.warp_row) ? 512 : 1024) / s.threads);
   return s;
 }
 int norm_grid(const Shape& s, long long N, int sms) {
   return (int)std::min<long long>(cdiv(N, s.rows_per_block), (long long)sms * s.per_sm);
 }
-// Stages that fit, and the block's dynamic shared memory (`least`: bytes the
-// kernel needs there in any case).
+// Ring stages that fit.
 int norm_stages(const Shape& s, size_t row_bytes) {
   const size_t fit = kRingBytes / s.per_sm / (row_bytes * s.rows_per_block);
   return (int)std::max<size_t>(2, std::min<size_t>(kNormStagesMax, fit));
@@ -108,11 +109,8 @@ KernelFn pick_fwd(const Shape& s) {
 }
 template <class XT, class DT, class WT>
 KernelFn pick_bwd3(const Shape& s) {
-  if (s.warp_row)
-    return s.nv == 1 ? k_norm_bwd<true, XT, DT, WT, 1, 256> : k_norm_bwd<true, XT, DT, WT, 2, 256>;
-  if (s.nv == 1) return k_norm_bwd<false, XT, DT, WT, 1, 256>;
-  return s.threads <= 256 ? k_norm_bwd<false, XT, DT, WT, 2, 256>
-                          : k_norm_bwd<false, XT, DT, WT, 2, 512>;
+  if (s.warp_row) return s.nv == 1 ? k_norm_bwd<true, XT, DT, WT, 1> : k_norm_bwd<true, XT, DT, WT, 2>;
+  return s.nv == 1 ? k_norm_bwd<false, XT, DT, WT, 1> : k_norm_bwd<false, XT, DT, WT, 2>;
 }
 template <class XT, class DT>
 KernelFn pick_bwd2(const fckl_norm_problem* p, const Shape& s) {
@@ -171,7 +169,7 @@ fckl_status fckl_block_norm_fwd(const fckl_norm_problem* prob, const void* x, co
                         : (wb ? pick_fwd<float, __nv_bfloat16>(s) : pick_fwd<float, float>(s));
   if (!allow_smem(k)) return FCKL_ERR_CUDA;
   const int grid = norm_grid(s, prob->N, sms);
-  const size_t row_bytes = (size_t)prob->H * ((xb ? 2 : 4) + (block ? 2 : 0));
+  const size_t row_bytes = (size_t)s.padded * ((xb ? 2 : 4) + (block ? 2 : 0));
   a.stages = norm_stages(s, row_bytes);
   const bool pdl = pdl_enabled();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -213,7 +211,7 @@ fckl_status fckl_block_norm_bwd(const fckl_norm_problem* prob, const void* x, co
   const KernelFn k = xb ? pick_bwd1<__nv_bfloat16>(prob, s) : pick_bwd1<float>(prob, s);
   if (!allow_smem(k)) return FCKL_ERR_CUDA;
   const int grid = norm_grid(s, prob->N, std::min(sms, kSms));  // the workspace's partials
-  const size_t row_bytes = (size_t)prob->H * ((xb ? 2 : 4) * (dv ? 2 : 1) + (block ? 2 : 0) +
+  const size_t row_bytes = (size_t)s.padded * ((xb ? 2 : 4) * (dv ? 2 : 1) + (block ? 2 : 0) +
                                               (dy ? (prob->dy_type == FCKL_BFLOAT ? 2 : 4) : 0));
   a.stages = norm_stages(s, row_bytes);
   size_t smem = a.stages * row_bytes * s.rows_per_block;

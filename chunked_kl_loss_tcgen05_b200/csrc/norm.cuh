@@ -8,15 +8,22 @@
 // With n = b rho_b (b without a post-norm), c = s g w1 and P = sum_r dv n:
 //   v = x + c n,  dw1 = s g P,  dg = s w1 P,
 // so the backward keeps two column sums, P and dw2, in registers.
-// All in fp32 from the inputs on (v is not rounded before it is normed; the
-// backward forms v again from x and b), each output rounded once.
+// and, dv being dv_in + k1 t - k2 v for two scalars k1, k2 of the row, the mean
+// that db needs is a combination of three sums that need neither:
+//   sum c n dv = sum c n dv_in + k1 sum c n t - k2 sum c n v.
+// All in fp32, two values to an instruction, from the inputs on (v is not
+// rounded before it is normed; the backward forms v again from x and b), each
+// output rounded once.
 //
 // Bound by HBM: forward x, b in and v, y out; backward x, b, dy, dv in and dx,
 // db out.  Rows go through a ring of shared-memory stages filled by 16-byte
 // asynchronous copies, several rows ahead; a thread copies exactly the values
 // it will read, so the data needs no barrier, and the waits are the copies'
 // own.  A row of more than 512 values takes a block, a shorter one a warp
-// (eight rows a block, and no barriers for the row sums either).
+// (eight rows a block).  What limits the kernels below HBM speed is latency, of
+// shuffles and barriers first: so all sums of a row go through one reduction,
+// which also carries the next row's sum of b^2 (the only one that has to come
+// before the others), and several values share a reduction's shuffles.
 #pragma once
 
 #include "ptx.cuh"
@@ -54,37 +61,62 @@ struct NormArgs {
   float* dw2;
 };
 
-// Sums of K values over the row's threads, the same on each of them.  `red` has
-// room for two calls (`turn` alternates), so one barrier per call is enough.
+// Sums of K (2 or 8) values over the row's threads, the same on each of them.
+// Lanes first split the values among them (xor 16, 8, 4: half of the values go
+// to the partner), then finish one each.  `red` has room for two calls (`turn`
+// alternates), so one barrier per call is enough; it starts zeroed, for the
+// warps a block does not have.
+constexpr int kNormRed = 2 * 8 * 16;
 template <bool kWarpRow, int K>
 __device__ __forceinline__ void row_sums(float (&s)[K], float* red, int& turn) {
+  static_assert(K == 2 || K == 8, "values per reduction");
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 0; k < K; ++k) s[k] = warp_sum(s[k]);
-  if (kWarpRow) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  float* r = red + (turn & 1) * 64;
-  ++turn;
-  if (lane == 0)
+  for (int n = K / 2, m = 16; n >= 1; n /= 2, m /= 2) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) r[k * 32 + warp] = s[k];
-  __syncthreads();
+    for (int i = 0; i < n; ++i) {
+      const bool up = lane & m;
+      const float keep = up ? s[i + n] : s[i], give = up ? s[i] : s[i + n];
+      s[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+    }
+  }
+  constexpr int kGroup = 32 / K;  // lanes that now share value lane / kGroup
+  float x = s[0];
 #pragma unroll
-  for (int k = 0; k < K; ++k) s[k] = warp_sum(lane < warps ? r[k * 32 + lane] : 0.f);
+  for (int m = kGroup / 2; m >= 1; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+  if constexpr (!kWarpRow) {
+    float* r = red + (turn & 1) * (kNormRed / 2);
+    ++turn;
+    if (lane % kGroup == 0) r[lane / kGroup * 16 + (threadIdx.x >> 5)] = x;
+    __syncthreads();
+    // value lane / kGroup: the group's lanes add its 16 warps' parts
+    const float* q = r + lane / kGroup * 16;
+    if constexpr (K == 8) {
+      const float4 f = reinterpret_cast<const float4*>(q)[lane % kGroup];
+      x = (f.x + f.y) + (f.z + f.w);
+    } else {
+      x = q[lane % kGroup];
+    }
+#pragma unroll
+    for (int m = kGroup / 2; m >= 1; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) s[k] = __shfl_sync(0xffffffffu, x, k * kGroup);
 }
 
 // Eight weights (+ offset), or ones.
 template <class WT>
-__device__ __forceinline__ void load_weight(const void* w, int col, float offset, float (&o)[8]) {
+__device__ __forceinline__ void load_weight(const void* w, int col, float offset, float2 (&o)[4]) {
   if (w == nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = 1.f;
+    for (int i = 0; i < 4; ++i) o[i] = both(1.f);
     return;
   }
   Raw8<WT> r;
   r.load(static_cast<const WT*>(w) + col);
   r.get(o);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] += offset;
+  for (int i = 0; i < 4; ++i) { o[i].x += offset; o[i].y += offset; }
 }
 
 // Eight values of T, global -> shared, asynchronously.
@@ -101,15 +133,15 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// The oldest of `stages` groups has landed.
-__device__ __forceinline__ void copy_wait_oldest(int stages) {
-  if (stages >= 4) copy_wait<3>();
-  else if (stages == 3) copy_wait<2>();
-  else copy_wait<1>();
+// All but the newest `stages` - 2 groups have landed.
+__device__ __forceinline__ void copy_wait_two(int stages) {
+  if (stages >= 4) copy_wait<2>();
+  else if (stages == 3) copy_wait<1>();
+  else copy_wait<0>();
 }
 constexpr int kNormStagesMax = 4;
 
-// Where a thread's row begins and how the rows are dealt.
+// A thread's place in its row, and how the rows are dealt.
 template <bool kWarpRow>
 struct NormRows {
   int tid, threads;      // within the row
@@ -126,248 +158,287 @@ struct NormRows {
   }
 };
 
-// NV vectors of eight per thread: columns 8 (tid + k threads).
-template <bool kWarpRow, class XT, class WT, int NV>
-__global__ void __launch_bounds__(512) k_norm_fwd(const NormArgs a) {
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float red[128];
-  pdl_wait();
-  pdl_trigger();
-  const int nvec = a.H / 8;
-  const float invH = 1.f / (float)a.H;
-  const NormRows<kWarpRow> rows;
-  const int row_bytes = a.H * ((int)sizeof(XT) + (a.b ? 2 : 0));
-  uint8_t* mine = ring + (kWarpRow ? (threadIdx.x >> 5) * a.stages * row_bytes : 0);
-  float c[NV][8], w2[NV][8];
+// The ring: per stage the row's values of x, b, dv and dy one after another,
+// each padded to all of the row's threads.  Threads past the row's end never
+// copy; their places are zeroed once, so they read zeros.
+template <class XT, class DT>
+struct NormRing {
+  uint8_t* base;
+  int stages, off_b, off_dv, off_dy, bytes;
+  __device__ __forceinline__ NormRing(uint8_t* ring, const NormArgs& a, int padded, int which)
+      : stages(a.stages) {
+    off_b = padded * (int)sizeof(XT);
+    off_dv = off_b + (a.b ? padded * 2 : 0);
+    off_dy = off_dv + (a.dv ? padded * (int)sizeof(XT) : 0);
+    bytes = off_dy + (a.dy ? padded * (int)sizeof(DT) : 0);
+    base = ring + which * stages * bytes;
+  }
+};
+
+// Zeros for this thread's eight values at `col` of every stage.
+template <class XT, class DT>
+__device__ __forceinline__ void ring_zero(const NormRing<XT, DT>& g, const NormArgs& a, int col) {
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  for (int s = 0; s < g.stages; ++s) {
+    uint8_t* p = g.base + s * g.bytes;
+    for (int i = 0; i < (int)sizeof(XT) / 2; ++i) {
+      reinterpret_cast<uint4*>(p + col * sizeof(XT))[i] = z;
+      if (a.dv) reinterpret_cast<uint4*>(p + g.off_dv + col * sizeof(XT))[i] = z;
+    }
+    if (a.b) *reinterpret_cast<uint4*>(p + g.off_b + col * 2) = z;
+    if (a.dy)
+      for (int i = 0; i < (int)sizeof(DT) / 2; ++i)
+        reinterpret_cast<uint4*>(p + g.off_dy + col * sizeof(DT))[i] = z;
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void get8(const uint8_t* s, int col, float2 (&v)[4]) {
+  Raw8<T> r;
+  r.load(reinterpret_cast<const T*>(s) + col);
+  r.get(v);
+}
+__device__ __forceinline__ void zero8(float2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = both(0.f);
+}
+
+// What both directions keep per column: c = s g w1 and w2.
+template <class WT, int NV>
+__device__ __forceinline__ void norm_weights(const NormArgs& a, int tid, int threads,
+                                             float2 (&c)[NV][4], float2 (&w2)[NV][4]) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int j = rows.tid + k * rows.threads;
+    const int col = 8 * (tid + k * threads);
+    zero8(c[k]);
+    zero8(w2[k]);
+    if (col >= a.H) continue;
+    float2 g[4];
+    load_weight<WT>(a.post ? a.w1 : nullptr, col, a.offset, c[k]);
+    load_weight<WT>(a.g, col, 0.f, g);
+    load_weight<WT>(a.w2, col, a.offset, w2[k]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[k][i] = w2[k][i] = 0.f;
-    if (j >= nvec) continue;
-    float g[8];
-    load_weight<WT>(a.post ? a.w1 : nullptr, 8 * j, a.offset, c[k]);
-    load_weight<WT>(a.g, 8 * j, 0.f, g);
-    load_weight<WT>(a.w2, 8 * j, a.offset, w2[k]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[k][i] *= a.scale * g[i];
+    for (int i = 0; i < 4; ++i) c[k][i] = mul2(c[k][i], mul2(both(a.scale), g[i]));
   }
+}
+
+// NV vectors of eight per thread: columns 8 (tid + k threads).
+template <bool kWarpRow, class XT, class WT, int NV>
+__global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : NV == 1 ? 2 : 1)
+    k_norm_fwd(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) float red[kNormRed];
+  pdl_wait();
+  pdl_trigger();
+  const float invH = 1.f / (float)a.H;
+  const NormRows<kWarpRow> rows;
+  const NormRing<XT, float> g(ring, a, rows.threads * NV * 8, kWarpRow ? threadIdx.x >> 5 : 0);
+  float2 c[NV][4], w2[NV][4];
+  norm_weights<WT, NV>(a, rows.tid, rows.threads, c, w2);
+  for (int i = threadIdx.x; i < kNormRed; i += blockDim.x) red[i] = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (8 * (rows.tid + k * rows.threads) >= a.H) ring_zero(g, a, 8 * (rows.tid + k * rows.threads));
+  if constexpr (!kWarpRow) __syncthreads();
   auto fetch = [&](long long r, int stage) {
     if (r < a.N) {
       const long long o = r * a.H;
-      uint8_t* s = mine + stage * row_bytes;
+      uint8_t* s = g.base + stage * g.bytes;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int j = rows.tid + k * rows.threads;
-        if (j >= nvec) continue;
-        copy8(s + j * 8 * sizeof(XT), static_cast<const XT*>(a.x) + o + 8 * j);
-        if (a.b)
-          copy8(s + a.H * sizeof(XT) + j * 16, static_cast<const __nv_bfloat16*>(a.b) + o + 8 * j);
+        const int col = 8 * (rows.tid + k * rows.threads);
+        if (col >= a.H) continue;
+        copy8(s + col * sizeof(XT), static_cast<const XT*>(a.x) + o + col);
+        if (a.b) copy8(s + g.off_b + col * 2, static_cast<const __nv_bfloat16*>(a.b) + o + col);
       }
     }
     copy_commit();
   };
+  auto square_b = [&](int stage) {
+    float2 q = both(0.f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float2 b[4];
+      get8<__nv_bfloat16>(g.base + stage * g.bytes + g.off_b, 8 * (rows.tid + k * rows.threads), b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q = fma2(b[i], b[i], q);
+    }
+    return q.x + q.y;
+  };
   int turn = 0, stage = 0;
   for (int i = 0; i < a.stages; ++i) fetch(rows.r + i * rows.step, i);
+  float rho_b = 1.f;
+  if (a.post && rows.r < a.N) {
+    copy_wait_two(a.stages);
+    float s[2] = {square_b(0), 0.f};
+    row_sums<kWarpRow>(s, red, turn);
+    rho_b = rsqrtf(fmaf(s[0], invH, a.eps));
+  }
   for (long long r = rows.r; r < a.N; r += rows.step) {
+    copy_wait_two(a.stages);  // this row and the next one
+    const uint8_t* s = g.base + stage * g.bytes;
     const long long o = r * a.H;
-    copy_wait_oldest(a.stages);
-    const uint8_t* s = mine + stage * row_bytes;
-    float v[NV][8], b[NV][8], sb[1] = {0.f};
+    const int next = stage + 1 == a.stages ? 0 : stage + 1;
+    float2 v[NV][4], q = both(0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int j = rows.tid + k * rows.threads;
+      const int col = 8 * (rows.tid + k * rows.threads);
+      get8<XT>(s, col, v[k]);
+      if (a.b) {
+        float2 b[4];
+        get8<__nv_bfloat16>(s + g.off_b, col, b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] = b[k][i] = 0.f;
-      if (j < nvec) {
-        Raw8<XT> rx;
-        rx.load(reinterpret_cast<const XT*>(s) + 8 * j);
-        rx.get(v[k]);
-        if (a.b) {
-          Raw8<__nv_bfloat16> rb;
-          rb.load(reinterpret_cast<const __nv_bfloat16*>(s + a.H * sizeof(XT)) + 8 * j);
-          rb.get(b[k]);
-        }
+        for (int i = 0; i < 4; ++i) v[k][i] = fma2(c[k][i], mul2(b[i], both(rho_b)), v[k][i]);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sb[0] = fmaf(b[k][i], b[k][i], sb[0]);
+      for (int i = 0; i < 4; ++i) q = fma2(v[k][i], v[k][i], q);
     }
+    float sums[2] = {q.x + q.y, a.post && r + rows.step < a.N ? square_b(next) : 0.f};
     fetch(r + a.stages * rows.step, stage);  // this thread has read its part of the stage
-    stage = stage + 1 == a.stages ? 0 : stage + 1;
-    if (a.b) {
-      float rho = 1.f;
-      if (a.post) {
-        row_sums<kWarpRow>(sb, red, turn);
-        rho = rsqrtf(fmaf(sb[0], invH, a.eps));
-      }
+    stage = next;
+    if (a.v) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int j = rows.tid + k * rows.threads;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] = fmaf(c[k][i], b[k][i] * rho, v[k][i]);
-        if (a.v && j < nvec) store8(static_cast<XT*>(a.v) + o + 8 * j, v[k]);
+        const int col = 8 * (rows.tid + k * rows.threads);
+        if (col < a.H) store8(static_cast<XT*>(a.v) + o + col, v[k]);
       }
     }
+    row_sums<kWarpRow>(sums, red, turn);
+    rho_b = a.post ? rsqrtf(fmaf(sums[1], invH, a.eps)) : 1.f;
     if (!a.pre) continue;
-    float sv[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sv[0] = fmaf(v[k][i], v[k][i], sv[0]);
-    row_sums<kWarpRow>(sv, red, turn);
-    const float rho = rsqrtf(fmaf(sv[0], invH, a.eps));
+    const float rho = rsqrtf(fmaf(sums[0], invH, a.eps));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int j = rows.tid + k * rows.threads;
-      if (j >= nvec) continue;
+      const int col = 8 * (rows.tid + k * rows.threads);
+      if (col >= a.H) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] *= rho * w2[k][i];
-      store8(static_cast<__nv_bfloat16*>(a.y) + o + 8 * j, v[k]);
+      for (int i = 0; i < 4; ++i) v[k][i] = mul2(mul2(v[k][i], both(rho)), w2[k][i]);
+      store8(static_cast<__nv_bfloat16*>(a.y) + o + col, v[k]);
     }
   }
   copy_wait<0>();
 }
 
-template <bool kWarpRow, class XT, class DT, class WT, int NV, int kThreads>
-__global__ void __launch_bounds__(kThreads, 512 / kThreads) k_norm_bwd(const NormArgs a) {
+template <bool kWarpRow, class XT, class DT, class WT, int NV>
+__global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : 1)
+    k_norm_bwd(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float red[128];
+  __shared__ __align__(16) float red[kNormRed];
   pdl_wait();
   pdl_trigger();
-  const int nvec = a.H / 8;
   const float invH = 1.f / (float)a.H;
   const NormRows<kWarpRow> rows;
-  const int off_b = a.H * (int)sizeof(XT), off_dv = off_b + (a.b ? a.H * 2 : 0);
-  const int off_dy = off_dv + (a.dv ? a.H * (int)sizeof(XT) : 0);
-  const int row_bytes = off_dy + (a.pre ? a.H * (int)sizeof(DT) : 0);
-  uint8_t* mine = ring + (kWarpRow ? (threadIdx.x >> 5) * a.stages * row_bytes : 0);
-  float c[NV][8], w2[NV][8], P[NV][8], D[NV][8];
+  const NormRing<XT, DT> g(ring, a, rows.threads * NV * 8, kWarpRow ? threadIdx.x >> 5 : 0);
+  float2 c[NV][4], w2[NV][4], P[NV][4], D[NV][4];
+  norm_weights<WT, NV>(a, rows.tid, rows.threads, c, w2);
+  for (int i = threadIdx.x; i < kNormRed; i += blockDim.x) red[i] = 0.f;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int j = rows.tid + k * rows.threads;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[k][i] = w2[k][i] = P[k][i] = D[k][i] = 0.f;
-    if (j >= nvec) continue;
-    float g[8];
-    load_weight<WT>(a.post ? a.w1 : nullptr, 8 * j, a.offset, c[k]);
-    load_weight<WT>(a.g, 8 * j, 0.f, g);
-    load_weight<WT>(a.w2, 8 * j, a.offset, w2[k]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[k][i] *= a.scale * g[i];
+    zero8(P[k]);
+    zero8(D[k]);
+    if (8 * (rows.tid + k * rows.threads) >= a.H) ring_zero(g, a, 8 * (rows.tid + k * rows.threads));
   }
+  if constexpr (!kWarpRow) __syncthreads();
   auto fetch = [&](long long r, int stage) {
     if (r < a.N) {
       const long long o = r * a.H;
-      uint8_t* s = mine + stage * row_bytes;
+      uint8_t* s = g.base + stage * g.bytes;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int j = rows.tid + k * rows.threads;
-        if (j >= nvec) continue;
-        copy8(s + j * 8 * sizeof(XT), static_cast<const XT*>(a.x) + o + 8 * j);
-        if (a.b) copy8(s + off_b + j * 16, static_cast<const __nv_bfloat16*>(a.b) + o + 8 * j);
-        if (a.dv)
-          copy8(s + off_dv + j * 8 * sizeof(XT), static_cast<const XT*>(a.dv) + o + 8 * j);
-        if (a.pre)
-          copy8(s + off_dy + j * 8 * sizeof(DT), static_cast<const DT*>(a.dy) + o + 8 * j);
+        const int col = 8 * (rows.tid + k * rows.threads);
+        if (col >= a.H) continue;
+        copy8(s + col * sizeof(XT), static_cast<const XT*>(a.x) + o + col);
+        if (a.b) copy8(s + g.off_b + col * 2, static_cast<const __nv_bfloat16*>(a.b) + o + col);
+        if (a.dv) copy8(s + g.off_dv + col * sizeof(XT), static_cast<const XT*>(a.dv) + o + col);
+        if (a.dy) copy8(s + g.off_dy + col * sizeof(DT), static_cast<const DT*>(a.dy) + o + col);
       }
     }
     copy_commit();
   };
+  auto square_b = [&](int stage) {
+    float2 q = both(0.f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float2 b[4];
+      get8<__nv_bfloat16>(g.base + stage * g.bytes + g.off_b, 8 * (rows.tid + k * rows.threads), b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q = fma2(b[i], b[i], q);
+    }
+    return q.x + q.y;
+  };
   int turn = 0, stage = 0;
   for (int i = 0; i < a.stages; ++i) fetch(rows.r + i * rows.step, i);
+  float rho_b = 1.f;
+  if (a.post && rows.r < a.N) {
+    copy_wait_two(a.stages);
+    float s[2] = {square_b(0), 0.f};
+    row_sums<kWarpRow>(s, red, turn);
+    rho_b = rsqrtf(fmaf(s[0], invH, a.eps));
+  }
   for (long long r = rows.r; r < a.N; r += rows.step) {
+    copy_wait_two(a.stages);  // this row and the next one
+    const uint8_t* s = g.base + stage * g.bytes;
     const long long o = r * a.H;
-    copy_wait_oldest(a.stages);
-    const uint8_t* s = mine + stage * row_bytes;
-    float v[NV][8], b[NV][8], d[NV][8];  // d: dy, then dv
-    float sb[1] = {0.f};
+    const int next = stage + 1 == a.stages ? 0 : stage + 1;
+    // With one vector a thread, the row's b, dy and dv stay in registers; with
+    // two they are read from the ring again after the reduction (in registers
+    // they would spill), which therefore refills the stage later.
+    constexpr bool kKeep = NV == 1;
+    float2 v[NV][4], n[kKeep ? NV : 1][4], dy[kKeep ? NV : 1][4], dv[kKeep ? NV : 1][4];
+    float2 qv = both(0.f), qt = both(0.f), q1 = both(0.f), q2 = both(0.f), q3 = both(0.f);
+    auto load = [&](int col, float2 (&bb)[4], float2 (&yy)[4], float2 (&vv)[4]) {
+      if (a.b) get8<__nv_bfloat16>(s + g.off_b, col, bb); else zero8(bb);
+      if (a.dy) get8<DT>(s + g.off_dy, col, yy); else zero8(yy);
+      if (a.dv) get8<XT>(s + g.off_dv, col, vv); else zero8(vv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bb[i] = mul2(bb[i], both(rho_b));
+    };
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int j = rows.tid + k * rows.threads;
+      const int col = 8 * (rows.tid + k * rows.threads), h = kKeep ? k : 0;
+      get8<XT>(s, col, v[k]);
+      load(col, n[h], dy[h], dv[h]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[k][i] = 0.f;
-      if (a.b && j < nvec) {
-        Raw8<__nv_bfloat16> rb;
-        rb.load(reinterpret_cast<const __nv_bfloat16*>(s + off_b) + 8 * j);
-        rb.get(b[k]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sb[0] = fmaf(b[k][i], b[k][i], sb[0]);
-    }
-    float rho_b = 1.f;
-    if (a.post) {
-      row_sums<kWarpRow>(sb, red, turn);
-      rho_b = rsqrtf(fmaf(sb[0], invH, a.eps));
-    }
-    float s2[2] = {0.f, 0.f};  // sum v^2, sum v t
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int j = rows.tid + k * rows.threads;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] = d[k][i] = 0.f;
-      if (j < nvec) {
-        Raw8<XT> rx;
-        rx.load(reinterpret_cast<const XT*>(s) + 8 * j);
-        rx.get(v[k]);
-        if (a.pre) {
-          Raw8<DT> rd;
-          rd.load(reinterpret_cast<const DT*>(s + off_dy) + 8 * j);
-          rd.get(d[k]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        b[k][i] *= rho_b;  // normed from here on
-        v[k][i] = fmaf(c[k][i], b[k][i], v[k][i]);
-        s2[0] = fmaf(v[k][i], v[k][i], s2[0]);
-        s2[1] = fmaf(v[k][i], d[k][i] * w2[k][i], s2[1]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 m = mul2(c[k][i], n[h][i]), t = mul2(dy[h][i], w2[k][i]);
+        v[k][i].x += m.x; v[k][i].y += m.y;
+        qv = fma2(v[k][i], v[k][i], qv);
+        qt = fma2(v[k][i], t, qt);
+        q1 = fma2(m, dv[h][i], q1);
+        q2 = fma2(m, t, q2);
+        q3 = fma2(m, v[k][i], q3);
       }
     }
-    float rho_v = 0.f, corr = 0.f;
+    float sums[8] = {qv.x + qv.y, qt.x + qt.y, q1.x + q1.y, q2.x + q2.y, q3.x + q3.y,
+                     a.post && r + rows.step < a.N ? square_b(next) : 0.f, 0.f, 0.f};
+    if (kKeep) fetch(r + a.stages * rows.step, stage);  // this thread's part has been read
+    row_sums<kWarpRow>(sums, red, turn);
+    float k1 = 0.f, k2 = 0.f;
     if (a.pre) {
-      row_sums<kWarpRow>(s2, red, turn);
-      rho_v = rsqrtf(fmaf(s2[0], invH, a.eps));
-      corr = s2[1] * invH * rho_v * rho_v;
+      k1 = rsqrtf(fmaf(sums[0], invH, a.eps));
+      k2 = sums[1] * invH * k1 * k1 * k1;
     }
-    float sbt[1] = {0.f};
+    const float mean = a.post ? (sums[2] + k1 * sums[3] - k2 * sums[4]) * invH : 0.f;
+    const float mb = -rho_b * mean;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int j = rows.tid + k * rows.threads;
-      float dv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (a.dv && j < nvec) {
-        Raw8<XT> rv;
-        rv.load(reinterpret_cast<const XT*>(s + off_dv) + 8 * j);
-        rv.get(dv);
+      const int col = 8 * (rows.tid + k * rows.threads), h = kKeep ? k : 0;
+      if (!kKeep) load(col, n[h], dy[h], dv[h]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = mul2(dy[h][i], w2[k][i]);
+        D[k][i] = fma2(dy[h][i], mul2(v[k][i], both(k1)), D[k][i]);
+        dv[h][i] = fma2(both(-k2), v[k][i], fma2(both(k1), t, dv[h][i]));
+        P[k][i] = fma2(dv[h][i], n[h][i], P[k][i]);
+        n[h][i] = fma2(both(mb), n[h][i], mul2(both(rho_b), mul2(c[k][i], dv[h][i])));
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        D[k][i] = fmaf(d[k][i], v[k][i] * rho_v, D[k][i]);
-        d[k][i] = fmaf(rho_v, fmaf(d[k][i], w2[k][i], -v[k][i] * corr), dv[i]);
-        P[k][i] = fmaf(d[k][i], b[k][i], P[k][i]);
-      }
-      if (a.dx && j < nvec) store8(static_cast<XT*>(a.dx) + o + 8 * j, d[k]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        d[k][i] *= c[k][i];
-        sbt[0] = fmaf(b[k][i], d[k][i], sbt[0]);
-      }
+      if (col >= a.H) continue;
+      if (a.dx) store8(static_cast<XT*>(a.dx) + o + col, dv[h]);
+      if (a.db) store8(static_cast<__nv_bfloat16*>(a.db) + o + col, n[h]);
     }
-    fetch(r + a.stages * rows.step, stage);  // this thread has read its part of the stage
-    stage = stage + 1 == a.stages ? 0 : stage + 1;
-    if (!a.db) continue;
-    float mean = 0.f;
-    if (a.post) {
-      row_sums<kWarpRow>(sbt, red, turn);
-      mean = sbt[0] * invH;
-    }
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int j = rows.tid + k * rows.threads;
-      if (j >= nvec) continue;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[k][i] = rho_b * fmaf(-mean, b[k][i], d[k][i]);
-      store8(static_cast<__nv_bfloat16*>(a.db) + o + 8 * j, d[k]);
-    }
+    if (!kKeep) fetch(r + a.stages * rows.step, stage);
+    stage = next;
+    rho_b = a.post ? rsqrtf(fmaf(sums[5], invH, a.eps)) : 1.f;
   }
   copy_wait<0>();
   if (!a.dw1 && !a.dg && !a.dw2) return;
@@ -378,10 +449,10 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) k_norm_bwd(const Nor
     float* w = sum + (threadIdx.x >> 5) * 2 * a.H;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int j = rows.tid + k * rows.threads;
-      if (j >= nvec) continue;
-      store8(w + 8 * j, P[k]);
-      store8(w + a.H + 8 * j, D[k]);
+      const int col = 8 * (rows.tid + k * rows.threads);
+      if (col >= a.H) continue;
+      store8(w + col, P[k]);
+      store8(w + a.H + col, D[k]);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * a.H; i += blockDim.x) {
@@ -392,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) k_norm_bwd(const Nor
   } else {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int j = rows.tid + k * rows.threads;
-      if (j >= nvec) continue;
-      store8(p + 8 * j, P[k]);
-      store8(p + a.H + 8 * j, D[k]);
+      const int col = 8 * (rows.tid + k * rows.threads);
+      if (col >= a.H) continue;
+      store8(p + col, P[k]);
+      store8(p + a.H + col, D[k]);
     }
   }
 }
