@@ -78,8 +78,8 @@ CeLayout ce_layout(const fckl_ce_problem* p, bool grads) {
   L.off_kw = take(C * 4);
   L.off_zlab = take(C * 4);
   L.off_lse2 = take(C * 4);
-  L.off_part = take(C * L.NT * sizeof(float2));
-  L.off_zsum = take(p->label_smoothing > 0.f ? C * L.NT * 4 : 0);
+  L.off_part = take(C * 2 * L.NT * sizeof(float2));
+  L.off_zsum = take(p->label_smoothing > 0.f ? C * 2 * L.NT * 4 : 0);
   L.off_h = take(align_up(C, CM) * p->H * 2);
   L.off_dlog = take(grads ? C * L.Vp * 2 : 0);
   // S segments of MT row tiles fit when S * MT * NTh <= slab_units
@@ -172,7 +172,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
   const float invT = 1.f / prob->T, scale2 = kLog2e / prob->T;
   const CtlArgs ca{ctl, wait_timeout_ns(), 0};
   const int pairs = dev->sms / 2;
-  const int NT = (int)L.NT, NTh = (int)L.NTh;
+  const int NT = (int)L.NT, NTh = (int)L.NTh, NP = 2 * NT;  // log-sum-exp partials of 128 columns
   const int KBh = (int)cdiv(H, BK), KBv = (int)cdiv(V, BK);
   const int narrow_h = (H % BN != 0 && H % BN <= 128) ? 1 : 0;
   const bool smooth = prob->label_smoothing > 0.f;
@@ -244,22 +244,22 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     const float* zs = smooth ? zsum : nullptr;
     // The GEMM over h W^T: its row count, hence its work, is read on the device.
 #define FCKL_CE_GEMM(Epi, map, params)                                                       \
-  FCKL_LAUNCH((gemm_pair_kernel<Epi, false, false>), Gv, GEMM_THREADS, pair_smem_bytes<Epi>(), \
+  FCKL_LAUNCH((gemm_pair_kernel<Epi, false, false>), Gv, gemm_threads<Epi>(), pair_smem_bytes<Epi>(), \
               mapH_k, mapW_k, map, params, sa_v, ca)
     if (q.mode == CeMode::kFwd) {
       {
         ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + nr * NT * 8.0);
         if (smooth) {
-          EpiCe<true>::Params pf{V, NT, scale2, lab, zlab, part, zsum};
+          EpiCe<true>::Params pf{V, NP, scale2, lab, zlab, part, zsum};
           FCKL_CE_GEMM(EpiCe<true>, mapW_k, pf);
         } else {
-          EpiCe<false>::Params pf{V, NT, scale2, lab, zlab, part, nullptr};
+          EpiCe<false>::Params pf{V, NP, scale2, lab, zlab, part, nullptr};
           FCKL_CE_GEMM(EpiCe<false>, mapW_k, pf);
         }
       }
       ProfScope ps(K_MERGE, st, 0.0, nr * (NT * 8.0 + 28.0));
       FCKL_LAUNCH(k_ce_merge, (int)cdiv(cap, kCeWarps), kCeWarps * 32, 0, (const float2*)part, zs,
-                  NT, rc, cap, V, invT, prob->label_smoothing, prob->z_loss, clist,
+                  NP, rc, cap, V, invT, prob->label_smoothing, prob->z_loss, clist,
                   (const float*)zlab, (const float*)kw, q.row_loss, q.lse_out, share + row0);
       continue;
     }
@@ -267,15 +267,15 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       {
         ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
         if (smooth) {
-          EpiCeStore<true>::Params pf{V, NT, scale2, lab, zlab, part, zsum, cap};
+          EpiCeStore<true>::Params pf{V, NP, scale2, lab, zlab, part, zsum, cap};
           FCKL_CE_GEMM(EpiCeStore<true>, mapD_st, pf);
         } else {
-          EpiCeStore<false>::Params pf{V, NT, scale2, lab, zlab, part, nullptr, cap};
+          EpiCeStore<false>::Params pf{V, NP, scale2, lab, zlab, part, nullptr, cap};
           FCKL_CE_GEMM(EpiCeStore<false>, mapD_st, pf);
         }
       }
       ProfScope ps(K_CE_SCALE, st, 0.0, nr * (V * 4.0 + NT * 16.0));
-      FCKL_LAUNCH(k_ce_dlogits, cap, 256, 0, (const float2*)part, zs, NT, rc, V, L.Vp, invT,
+      FCKL_LAUNCH(k_ce_dlogits, cap, 256, 0, (const float2*)part, zs, NP, rc, V, L.Vp, invT,
                   prob->label_smoothing, prob->z_loss, clist, (const int*)lab, (const float*)zlab,
                   (const float*)kw, reinterpret_cast<uint4*>(dlog), q.row_loss, q.lse_out,
                   share + row0);
@@ -292,7 +292,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
                      L.slab_units};
       EpiCeDH::Params ph{H, invT, ctl};
       ProfScope ps(K_DH, st, flops, 2.0 * nr * V + 2.0 * (double)V * H + 4.0 * nr * H);
-      FCKL_LAUNCH((gemm_pair_kernel<EpiCeDH, false, true>), 2 * pairs, GEMM_THREADS,
+      FCKL_LAUNCH((gemm_pair_kernel<EpiCeDH, false, true>), 2 * pairs, gemm_threads<EpiCeDH>(),
                   pair_smem_bytes<EpiCeDH>(), mapD_k, mapW_mn, mapSlab, ph, sa_h, ca);
     }
     // dW (+)= dlogits^T h: dlogits and the gathered rows were complete before
@@ -309,12 +309,12 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       if (dw_direct16) {
         EpiCeDW::Params pw{V, H, invT, ctl};
         FCKL_LAUNCH((gemm_pair_kernel<EpiCeDW, true, true>), grid_for((long long)MTv * NTh),
-                    GEMM_THREADS, pair_smem_bytes<EpiCeDW>(), mapD_mn, mapH_mn, mapdW, pw, sa_w,
+                    gemm_threads<EpiCeDW>(), pair_smem_bytes<EpiCeDW>(), mapD_mn, mapH_mn, mapdW, pw, sa_w,
                     ca);
       } else {
         EpiCeDWSum::Params pw{V, H, invT, c > 0 ? 1 : 0, ctl};
         FCKL_LAUNCH((gemm_pair_kernel<EpiCeDWSum, true, true>), grid_for((long long)MTv * NTh),
-                    GEMM_THREADS, pair_smem_bytes<EpiCeDWSum>(), mapD_mn, mapH_mn, mapdW, pw, sa_w, ca);
+                    gemm_threads<EpiCeDWSum>(), pair_smem_bytes<EpiCeDWSum>(), mapD_mn, mapH_mn, mapdW, pw, sa_w, ca);
       }
     }
     // the last chunk's blocks zero dW when no row was kept

@@ -152,181 +152,197 @@ __global__ void __launch_bounds__(128)
 }
 
 // ---------------------------------------------------------------- epilogues
-// Forward: per row and vocab tile of 256 columns, (max, sum 2^(a2 - max)) of
-// a2 = z log2(e) / T, z at the row's label if it lies in the tile, and (kSum)
-// the tile's sum of z for label smoothing.  The logits are not written.
+// All with eight warps: a thread owns one accumulator row and one half (128
+// columns) of the tile.  At H = 1024 a tile's main loop takes about 8000 cycles,
+// and four warps took longer than that over its exponentials, which come one a
+// cycle from each SM quarter's special-function unit only if two warps take
+// turns.  The half's results leave as partials of their own: [rows, NP], NP = 2
+// per vocab tile.  One 4 KB staging buffer a warp (as in epilogues.cuh) keeps
+// the operand stages' room.
+
+// Waits until the warp's staging buffer is no longer read by its last store.
+__device__ __forceinline__ void stage_reuse(int lane) {
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
+}
+
+// max over the first `cols` of 32 values, in four chains.
+__device__ __forceinline__ float max32(const float (&v)[32], int cols) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  if (cols >= 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) m[j & 3] = j < cols ? fmaxf(m[j & 3], v[j]) : m[j & 3];
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// v = 2^(v scale2 - ref) for the first `cols` values, 0 behind; returns the sum.
+__device__ __forceinline__ float exp32(float (&v)[32], float scale2, float ref, int cols) {
+  const float2 sc = both(scale2), mr = both(-ref);
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const float2 a = fma2(make_float2(v[j], v[j + 1]), sc, mr);
+    v[j] = ex2_approx(a.x);
+    v[j + 1] = ex2_approx(a.y);
+  }
+  if (cols < 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = j < cols ? v[j] : 0.f;
+  }
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) s[j & 3] += v[j];
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+__device__ __forceinline__ float sum32(const float (&v)[32], int cols) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) s[j & 3] += j < cols ? v[j] : 0.f;
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+__device__ __forceinline__ float pick32(const float (&v)[32], int at) {
+  float z = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) z = j == at ? v[j] : z;
+  return z;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Forward: per row and half tile, (max, sum 2^(a2 - max)) of a2 = z log2(e) / T,
+// z at the row's label if it lies in the half, and (kSum) the half's sum of z
+// for label smoothing.  The logits are not written.
 template <bool kSum>
 struct EpiCe {
+  static constexpr int kEpiWarps = 8;
   static constexpr uint32_t kSmemBytes = 0;
   static constexpr bool kUsesMapC = false;
   struct Params {
-    int V, NT;
+    int V, NP;
     float scale2;          // log2(e) / T
     const int* lab;        // [rows]
     float* zlab;           // [rows] z at the label
-    float2* partials;      // [rows, NT]
-    float* zsum;           // [rows, NT] (kSum)
+    float2* partials;      // [rows, NP]
+    float* zsum;           // [rows, NP] (kSum)
   };
   struct State {};
   static __device__ void init(const Params&, State&, uint8_t*, int) {}
   static __device__ void tile(const Params& p, State&, const Work& w, uint32_t taddr, int r,
                               const CUtensorMap*, int, int) {
-    const int row = w.m0 + r;
+    const int row = w.m0 + r, n0 = w.n0 + w.half * 128;
     const bool rv = row < w.rows;
-    const int y = rv ? __ldg(p.lab + row) - w.n0 : -1;  // label's column in the tile
+    const int y = rv ? __ldg(p.lab + row) - n0 : -1;  // label's column in the half
     float m = -INFINITY, s = 0.f, u = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < BN / 32; ++c) {
+    for (int c = 0; c < 4; ++c) {
       float v[32];
-      tmem_ld32_conv(taddr + (uint32_t)(c * 32), v);
-      if (!rv) continue;
-      const int base = w.n0 + c * 32;
-      if (base >= p.V) continue;
-      if ((y >> 5) == c) {
-        float z = 0.f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) z = (j == (y & 31)) ? v[j] : z;
-        p.zlab[row] = z;
-      }
-      if (kSum) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) u += base + j < p.V ? v[j] : 0.f;
-      }
-      if (base + 32 > p.V) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = (base + j < p.V) ? v[j] : -INFINITY;
-      }
-      float cz = v[0];
-#pragma unroll
-      for (int j = 1; j < 32; ++j) cz = fmaxf(cz, v[j]);
-      const float nm = fmaxf(m, cz * p.scale2);
+      tmem_ld32_conv(taddr + (uint32_t)(w.half * 128 + c * 32), v);
+      const int cols = rv ? p.V - (n0 + c * 32) : 0;
+      if (cols <= 0) continue;
+      if ((y >> 5) == c) p.zlab[row] = pick32(v, y & 31);
+      if (kSum) u += sum32(v, cols);
+      const float nm = fmaxf(m, max32(v, cols) * p.scale2);
       const float ref = nm == -INFINITY ? 0.f : nm;  // a slice of -inf only adds 0, not NaN
-      float acc = 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) acc += ex2_approx(fmaf(v[j], p.scale2, -ref));
-      s = s * ex2_approx(m - ref) + acc;
+      s = s * ex2_approx(m - ref) + exp32(v, p.scale2, ref, cols);
       m = nm;
     }
+    const int t = 2 * w.nt + w.half;
     if (rv) {
-      p.partials[(size_t)row * p.NT + w.nt] = make_float2(m, s);
-      if (kSum) p.zsum[(size_t)row * p.NT + w.nt] = u;
+      p.partials[(size_t)row * p.NP + t] = make_float2(m, s);
+      if (kSum) p.zsum[(size_t)row * p.NP + t] = u;
     }
   }
   static __device__ void finish(const Params&, State&, int) {}
 };
 
 // Forward of a call that also wants gradients: as EpiCe, and the exponentials
-// themselves are kept, E = 2^(a2 - m) per tile with m = (the row's tile maximum)
-// - 15, as fp16 in the chunk's [rows, Vp] block; k_ce_dlogits turns them into
-// dlogits in place once the row's LSE is known.  So the backward needs no second
-// logits product (6 H V flops per row instead of 8, for 4 V more bytes: at
-// H = 4096 the product costs about 10 times what the bytes do).
+// themselves are kept, E = 2^(a2 - m) per half tile with m = (the row's maximum
+// in it) - 15, as fp16 in the chunk's [rows, Vp] block; k_ce_dlogits turns them
+// into dlogits in place once the row's LSE is known.  So the backward needs no
+// second logits product (6 H V flops per row instead of 8, for 4 V more bytes:
+// at H = 4096 the product costs about 10 times what the bytes do).
 // fp16 because E is rounded here and G once more in k_ce_dlogits: 2^-11 against
 // G's own 2^-8; in bf16 the two roundings would add up.  With the offset of 15
-// the tile's largest E is 2^15 and E stays normal down to 2^-29 of it.
+// the largest E is 2^15 and E stays normal down to 2^-29 of it.
 // The accumulator is read twice (maximum, then exponentials).
 template <bool kSum>
 struct EpiCeStore {
-  static constexpr uint32_t kSmemBytes = 4 * 2 * 4096;
+  static constexpr int kEpiWarps = 8;
+  static constexpr uint32_t kSmemBytes = 8 * 4096;
   static constexpr bool kUsesMapC = true;  // map C: [rows, Vp] 16-bit, box {64, 32}
   struct Params {
-    int V, NT;
+    int V, NP;
     float scale2;
     const int* lab;
     float* zlab;
-    float2* partials;      // [rows, NT] (m, sum of E before rounding)
+    float2* partials;      // [rows, NP] (m, sum of E before rounding)
     float* zsum;
-    int store_rows;
+    int store_rows;        // rows of the store map
   };
   struct State {
-    int n;
     uint8_t* buf;
   };
   static __device__ void init(const Params&, State& st, uint8_t* smem_warp, int) {
-    st.n = 0; st.buf = smem_warp;
-  }
-  static __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  static __device__ __forceinline__ void exps(float (&v)[32], float scale2, float ref, int cols,
-                                              float& sum) {
-    if (cols >= 32) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = ex2_approx(fmaf(v[j], scale2, -ref));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = j < cols ? ex2_approx(fmaf(v[j], scale2, -ref)) : 0.f;
-    }
-    float acc = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) acc += v[j];
-    sum += acc;
+    st.buf = smem_warp;
   }
   static __device__ void tile(const Params& p, State& st, const Work& w, uint32_t taddr, int r,
                               const CUtensorMap* mapC, int quarter, int lane) {
-    const int row = w.m0 + r;
+    const int row = w.m0 + r, n0 = w.n0 + w.half * 128;
+    const uint32_t ta = taddr + (uint32_t)(w.half * 128);
     const bool rv = row < w.rows;
-    const int y = rv ? __ldg(p.lab + row) - w.n0 : -1;
+    const int y = rv ? __ldg(p.lab + row) - n0 : -1;
     float top = -INFINITY, u = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < BN / 32; ++c) {
+    for (int c = 0; c < 4; ++c) {
       float v[32];
-      tmem_ld32_conv(taddr + (uint32_t)(c * 32), v);
-      const int cols = rv ? p.V - (w.n0 + c * 32) : 0;
-      if ((y >> 5) == c) {
-        float z = 0.f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) z = (j == (y & 31)) ? v[j] : z;
-        p.zlab[row] = z;
-      }
-      if (kSum) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) u += j < cols ? v[j] : 0.f;
-      }
-      if (cols >= 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) top = j < cols ? fmaxf(top, v[j]) : top;
-      }
+      tmem_ld32_conv(ta + (uint32_t)(c * 32), v);
+      const int cols = rv ? p.V - (n0 + c * 32) : 0;
+      if ((y >> 5) == c) p.zlab[row] = pick32(v, y & 31);
+      if (kSum) u += sum32(v, cols);
+      top = fmaxf(top, max32(v, cols));
     }
     const float m = fmaf(top, p.scale2, -15.f);
-    const float ref = m == -INFINITY ? 0.f : m;  // a tile of -inf only adds 0, not NaN
+    const float ref = m == -INFINITY ? 0.f : m;  // a half of -inf only adds 0, not NaN
     float s = 0.f;
     const int y0 = w.m0 + quarter * 32;
+    // rows behind the last one, up to the next multiple of 64, are stored as
+    // zeros (the dW GEMM reads whole blocks of 64 rows)
     const int y_end = min((w.rows + 63) & ~63, p.store_rows);
 #pragma unroll 1
-    for (int c = 0; c < BN / 64; ++c) {
-      const int base = w.n0 + c * 64;
+    for (int c = 0; c < 2; ++c) {
+      const int base = n0 + c * 64;
       const int cols = rv ? p.V - base : 0;
-      float v0[32], v1[32];
-      tmem_ld32_conv(taddr + (uint32_t)(c * 64), v0);
-      tmem_ld32_conv(taddr + (uint32_t)(c * 64 + 32), v1);
-      exps(v0, p.scale2, ref, cols, s);
-      exps(v1, p.scale2, ref, cols - 32, s);
-      uint8_t* buf = st.buf + (st.n & 1) * 4096;
-      stage_acquire(lane);
+      stage_reuse(lane);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        *stage_chunk(buf, lane, j) = make_uint4(
-            pack_half2(v0[8 * j], v0[8 * j + 1]), pack_half2(v0[8 * j + 2], v0[8 * j + 3]),
-            pack_half2(v0[8 * j + 4], v0[8 * j + 5]), pack_half2(v0[8 * j + 6], v0[8 * j + 7]));
-        *stage_chunk(buf, lane, 4 + j) = make_uint4(
-            pack_half2(v1[8 * j], v1[8 * j + 1]), pack_half2(v1[8 * j + 2], v1[8 * j + 3]),
-            pack_half2(v1[8 * j + 4], v1[8 * j + 5]), pack_half2(v1[8 * j + 6], v1[8 * j + 7]));
+      for (int h = 0; h < 2; ++h) {
+        float v[32];
+        tmem_ld32_conv(ta + (uint32_t)(c * 64 + h * 32), v);
+        s += exp32(v, p.scale2, ref, cols - 32 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *stage_chunk(st.buf, lane, 4 * h + j) =
+              make_uint4(pack_half2(v[8 * j], v[8 * j + 1]), pack_half2(v[8 * j + 2], v[8 * j + 3]),
+                         pack_half2(v[8 * j + 4], v[8 * j + 5]),
+                         pack_half2(v[8 * j + 6], v[8 * j + 7]));
       }
       stage_release();
-      if (lane == 0) {
-        if (base < p.V && y0 < y_end) tma_store_2d(mapC, smem_u32(buf), base, y0);
+      if (lane == 0) {  // one group per slice, empty when the slice lies outside the map
+        if (base < p.V && y0 < y_end) tma_store_2d(mapC, smem_u32(st.buf), base, y0);
         bulk_commit();
       }
-      ++st.n;
     }
+    const int t = 2 * w.nt + w.half;
     if (rv) {
-      p.partials[(size_t)row * p.NT + w.nt] = make_float2(m, s);
-      if (kSum) p.zsum[(size_t)row * p.NT + w.nt] = u;
+      p.partials[(size_t)row * p.NP + t] = make_float2(m, s);
+      if (kSum) p.zsum[(size_t)row * p.NP + t] = u;
     }
   }
   static __device__ void finish(const Params&, State&, int lane) {
@@ -335,11 +351,13 @@ struct EpiCeStore {
   }
 };
 
-// Backward without the forward's exponentials (the row-gradient call): recomputed z tile -> G (see the top), rounded once to bf16 and
-// TMA-stored to the chunk's [rows, Vp] block.  Columns in [V, Vp) and the rows
-// behind the last one, up to the next multiple of 64, are stored as zeros.
+// Backward without the forward's exponentials (the row-gradient call):
+// recomputed z tile -> G (see the top), rounded once to bf16 and TMA-stored to
+// the chunk's [rows, Vp] block.  Columns in [V, Vp) and the rows behind the last
+// one, up to the next multiple of 64, are stored as zeros.
 struct EpiCeDlogits {
-  static constexpr uint32_t kSmemBytes = 4 * 2 * 4096;
+  static constexpr int kEpiWarps = 8;
+  static constexpr uint32_t kSmemBytes = 8 * 4096;
   static constexpr bool kUsesMapC = true;  // map C: [rows, Vp] bf16, box {64, 32}
   struct Params {
     int V;
@@ -352,63 +370,100 @@ struct EpiCeDlogits {
     int store_rows;        // rows of the store map
   };
   struct State {
-    int n;
     uint8_t* buf;
   };
   static __device__ void init(const Params&, State& st, uint8_t* smem_warp, int) {
-    st.n = 0; st.buf = smem_warp;
-  }
-  static __device__ __forceinline__ void slice(float (&v)[32], float scale2, float lse2, float kap,
-                                               float base_mass, float label_mass, int y, int cols) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float t = j == y ? base_mass + label_mass : base_mass;
-      const float g = fmaf(kap, ex2_approx(fmaf(v[j], scale2, -lse2)), -t);
-      v[j] = j < cols ? g : 0.f;
-    }
+    st.buf = smem_warp;
   }
   static __device__ void tile(const Params& p, State& st, const Work& w, uint32_t taddr, int r,
                               const CUtensorMap* mapC, int quarter, int lane) {
-    const int row = w.m0 + r;
+    const int row = w.m0 + r, n0 = w.n0 + w.half * 128;
+    const uint32_t ta = taddr + (uint32_t)(w.half * 128);
     const bool rv = row < w.rows;
     const float kw = rv ? p.kw[row] : 0.f;
     const float lse2 = rv ? p.lse2[row] : 0.f;
-    const int y = rv ? p.lab[row] - w.n0 : -1;
+    const int y = rv ? p.lab[row] - n0 : -1;
     const float kap = kw * fmaf(p.zloss2, lse2 * kLn2, 1.f);
     const float label_mass = kw * (1.f - p.smooth), base_mass = kw * p.smooth / (float)p.V;
     const int y0 = w.m0 + quarter * 32;
     const int y_end = min((w.rows + 63) & ~63, p.store_rows);
+    const float2 sc = both(p.scale2), ml = both(-lse2), kk = both(kap), nb = both(-base_mass);
 #pragma unroll 1
-    for (int s = 0; s < BN / 64; ++s) {
-      const int base = w.n0 + s * 64;
-      float v0[32], v1[32];
-      tmem_ld32_conv(taddr + (uint32_t)(s * 64), v0);
-      tmem_ld32_conv(taddr + (uint32_t)(s * 64 + 32), v1);
-      slice(v0, p.scale2, lse2, kap, base_mass, label_mass, y - s * 64, rv ? p.V - base : 0);
-      slice(v1, p.scale2, lse2, kap, base_mass, label_mass, y - s * 64 - 32,
-            rv ? p.V - base - 32 : 0);
-      uint8_t* buf = st.buf + (st.n & 1) * 4096;
-      stage_acquire(lane);
+    for (int c = 0; c < 2; ++c) {
+      const int base = n0 + c * 64;
+      stage_reuse(lane);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        *stage_chunk(buf, lane, j) = make_uint4(
-            pack_bf16x2(v0[8 * j], v0[8 * j + 1]), pack_bf16x2(v0[8 * j + 2], v0[8 * j + 3]),
-            pack_bf16x2(v0[8 * j + 4], v0[8 * j + 5]), pack_bf16x2(v0[8 * j + 6], v0[8 * j + 7]));
-        *stage_chunk(buf, lane, 4 + j) = make_uint4(
-            pack_bf16x2(v1[8 * j], v1[8 * j + 1]), pack_bf16x2(v1[8 * j + 2], v1[8 * j + 3]),
-            pack_bf16x2(v1[8 * j + 4], v1[8 * j + 5]), pack_bf16x2(v1[8 * j + 6], v1[8 * j + 7]));
+      for (int h = 0; h < 2; ++h) {
+        float v[32];
+        tmem_ld32_conv(ta + (uint32_t)(c * 64 + h * 32), v);
+        const int cols = rv ? p.V - base - 32 * h : 0, yc = y - c * 64 - 32 * h;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float2 a = fma2(make_float2(v[j], v[j + 1]), sc, ml);
+          const float2 g = fma2(kk, make_float2(ex2_approx(a.x), ex2_approx(a.y)), nb);
+          v[j] = g.x;
+          v[j + 1] = g.y;
+        }
+        if ((unsigned)yc < 32u) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = j == yc ? v[j] - label_mass : v[j];
+        }
+        if (cols < 32) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = j < cols ? v[j] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *stage_chunk(st.buf, lane, 4 * h + j) = make_uint4(
+              pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+              pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
       }
       stage_release();
-      if (lane == 0) {  // one group per slice, empty when the slice lies outside the map
-        if (base < p.V && y0 < y_end) tma_store_2d(mapC, smem_u32(buf), base, y0);
+      if (lane == 0) {
+        if (base < p.V && y0 < y_end) tma_store_2d(mapC, smem_u32(st.buf), base, y0);
         bulk_commit();
       }
-      ++st.n;
     }
   }
   static __device__ void finish(const Params&, State&, int lane) {
     if (lane == 0) bulk_wait_all();
     __syncwarp();
+  }
+};
+
+// What the three gradient epilogues share: alpha = 1 / (T D) and the staging.
+struct CeGradState {
+  float alpha;
+  uint8_t* buf;
+  __device__ void init(float invT, const DeviceCtl* ctl, uint8_t* smem_warp) {
+    const int nv = ctl->n_valid;
+    alpha = nv > 0 ? invT / (float)nv : 0.f;
+    buf = smem_warp;
+  }
+  // alpha * the half's accumulator as fp32, 32 columns at a time, to (x, y) of
+  // the map (stored, or added in place).
+  __device__ __forceinline__ void put_fp32(uint32_t ta, const CUtensorMap* map, bool add, int x0,
+                                           int x_end, int y, bool y_ok, int lane) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float v[32];
+      tmem_ld32_conv(ta + (uint32_t)(c * 32), v);
+      stage_reuse(lane);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *stage_chunk(buf, lane, j) =
+            make_uint4(__float_as_uint(alpha * v[4 * j]), __float_as_uint(alpha * v[4 * j + 1]),
+                       __float_as_uint(alpha * v[4 * j + 2]), __float_as_uint(alpha * v[4 * j + 3]));
+      stage_release();
+      const int x = x0 + c * 32;
+      if (lane == 0) {
+        if (x < x_end && y_ok) {
+          if (add) tma_reduce_add_2d(map, smem_u32(buf), x, y);
+          else tma_store_2d(map, smem_u32(buf), x, y);
+        }
+        bulk_commit();
+      }
+    }
   }
 };
 
@@ -416,30 +471,23 @@ struct EpiCeDlogits {
 // [ks * 256 * MT, ...) of the slab array), not added in place, so that the sum
 // over the segments has one order and repeated calls give the same bits.
 struct EpiCeDH {
-  static constexpr uint32_t kSmemBytes = 4 * 2 * 4096;
+  static constexpr int kEpiWarps = 8;
+  static constexpr uint32_t kSmemBytes = 8 * 4096;
   static constexpr bool kUsesMapC = true;  // map C: slabs [S * 256 * MT, H] fp32, box {32, 32}
   struct Params {
     int H;
     float invT;
     const DeviceCtl* ctl;
   };
-  struct State {
-    float alpha;
-    int n;
-    uint8_t* buf;
-  };
+  using State = CeGradState;
   static __device__ void init(const Params& p, State& st, uint8_t* smem_warp, int) {
-    const int nv = p.ctl->n_valid;
-    st.alpha = nv > 0 ? p.invT / (float)nv : 0.f;
-    st.n = 0;
-    st.buf = smem_warp;
+    st.init(p.invT, p.ctl, smem_warp);
   }
   static __device__ void tile(const Params& p, State& st, const Work& w, uint32_t taddr, int,
                               const CUtensorMap* mapC, int quarter, int lane) {
-    const int y = w.m0 + quarter * 32;
-    const int pitch = (w.rows + PM - 1) / PM * PM;
-    stage_fp32_slices<false>(st.buf, st.n, taddr, st.alpha, mapC, w.n0, p.H, w.ks * pitch + y,
-                             y < w.rows, lane);
+    const int y = w.m0 + quarter * 32, pitch = (w.rows + PM - 1) / PM * PM;
+    st.put_fp32(taddr + (uint32_t)(w.half * 128), mapC, false, w.n0 + w.half * 128, p.H,
+                w.ks * pitch + y, y < w.rows, lane);
   }
   static __device__ void finish(const Params&, State&, int lane) {
     if (lane == 0) bulk_wait_all();
@@ -447,61 +495,73 @@ struct EpiCeDH {
   }
 };
 
-// dW in fp32 over the chunks (a type of its own, so that the two translation
-// units instantiate different kernels).
-struct EpiCeDWSum : EpiDW {};
+// dW in fp32: stored by the first chunk, added to in place by later ones (one
+// tile a launch, so in the chunks' order).
+struct EpiCeDWSum {
+  static constexpr int kEpiWarps = 8;
+  static constexpr uint32_t kSmemBytes = 8 * 4096;
+  static constexpr bool kUsesMapC = true;  // map C: dW [V, H] fp32, box {32, 32}
+  struct Params {
+    int V, H;
+    float invT;
+    int accumulate;
+    const DeviceCtl* ctl;
+  };
+  using State = CeGradState;
+  static __device__ void init(const Params& p, State& st, uint8_t* smem_warp, int) {
+    st.init(p.invT, p.ctl, smem_warp);
+  }
+  static __device__ void tile(const Params& p, State& st, const Work& w, uint32_t taddr, int,
+                              const CUtensorMap* mapC, int quarter, int lane) {
+    const int y = w.m0 + quarter * 32;
+    st.put_fp32(taddr + (uint32_t)(w.half * 128), mapC, p.accumulate != 0, w.n0 + w.half * 128,
+                p.H, y, y < p.V, lane);
+  }
+  static __device__ void finish(const Params&, State&, int lane) {
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+};
 
 // dW written once, rounded once to bf16 (calls of one chunk).
 struct EpiCeDW {
-  static constexpr uint32_t kSmemBytes = 4 * 2 * 4096;
+  static constexpr int kEpiWarps = 8;
+  static constexpr uint32_t kSmemBytes = 8 * 4096;
   static constexpr bool kUsesMapC = true;  // map C: dW [V, H] bf16, box {64, 32}
   struct Params {
     int V, H;
     float invT;
     const DeviceCtl* ctl;
   };
-  struct State {
-    float alpha;
-    int n;
-    uint8_t* buf;
-  };
+  using State = CeGradState;
   static __device__ void init(const Params& p, State& st, uint8_t* smem_warp, int) {
-    const int nv = p.ctl->n_valid;
-    st.alpha = nv > 0 ? p.invT / (float)nv : 0.f;
-    st.n = 0;
-    st.buf = smem_warp;
+    st.init(p.invT, p.ctl, smem_warp);
   }
   static __device__ void tile(const Params& p, State& st, const Work& w, uint32_t taddr, int,
                               const CUtensorMap* mapC, int quarter, int lane) {
     const int y = w.m0 + quarter * 32;
+    const float al = st.alpha;
 #pragma unroll 1
-    for (int s = 0; s < BN / 64; ++s) {
-      float v0[32], v1[32];
-      tmem_ld32_conv(taddr + (uint32_t)(s * 64), v0);
-      tmem_ld32_conv(taddr + (uint32_t)(s * 64 + 32), v1);
-      uint8_t* buf = st.buf + (st.n & 1) * 4096;
-      stage_acquire(lane);
-      const float al = st.alpha;
+    for (int c = 0; c < 2; ++c) {
+      const int x = w.n0 + w.half * 128 + c * 64;
+      stage_reuse(lane);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        *stage_chunk(buf, lane, j) =
-            make_uint4(pack_bf16x2(al * v0[8 * j], al * v0[8 * j + 1]),
-                       pack_bf16x2(al * v0[8 * j + 2], al * v0[8 * j + 3]),
-                       pack_bf16x2(al * v0[8 * j + 4], al * v0[8 * j + 5]),
-                       pack_bf16x2(al * v0[8 * j + 6], al * v0[8 * j + 7]));
-        *stage_chunk(buf, lane, 4 + j) =
-            make_uint4(pack_bf16x2(al * v1[8 * j], al * v1[8 * j + 1]),
-                       pack_bf16x2(al * v1[8 * j + 2], al * v1[8 * j + 3]),
-                       pack_bf16x2(al * v1[8 * j + 4], al * v1[8 * j + 5]),
-                       pack_bf16x2(al * v1[8 * j + 6], al * v1[8 * j + 7]));
+      for (int h = 0; h < 2; ++h) {
+        float v[32];
+        tmem_ld32_conv(taddr + (uint32_t)(w.half * 128 + c * 64 + h * 32), v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *stage_chunk(st.buf, lane, 4 * h + j) =
+              make_uint4(pack_bf16x2(al * v[8 * j], al * v[8 * j + 1]),
+                         pack_bf16x2(al * v[8 * j + 2], al * v[8 * j + 3]),
+                         pack_bf16x2(al * v[8 * j + 4], al * v[8 * j + 5]),
+                         pack_bf16x2(al * v[8 * j + 6], al * v[8 * j + 7]));
       }
       stage_release();
-      const int x = w.n0 + s * 64;
       if (lane == 0) {
-        if (x < p.H && y < p.V) tma_store_2d(mapC, smem_u32(buf), x, y);
+        if (x < p.H && y < p.V) tma_store_2d(mapC, smem_u32(st.buf), x, y);
         bulk_commit();
       }
-      ++st.n;
     }
   }
   static __device__ void finish(const Params&, State&, int lane) {
@@ -516,7 +576,7 @@ struct EpiCeDW {
 // left-out rows) and their share k_r l_r of the loss (list order).  One warp
 // per row.
 __global__ void __launch_bounds__(kCeWarps * 32)
-    k_ce_merge(const float2* __restrict__ partials, const float* __restrict__ zsum, int NT,
+    k_ce_merge(const float2* __restrict__ partials, const float* __restrict__ zsum, int NP,
                RowCount rc, int cap, int V, float invT, float smooth, float zloss,
                const int32_t* __restrict__ list, const float* __restrict__ zlab,
                const float* __restrict__ kw, float* __restrict__ row_loss,
@@ -535,15 +595,15 @@ __global__ void __launch_bounds__(kCeWarps * 32)
     }
     return;
   }
-  const float2* pr = partials + (size_t)row * NT;
+  const float2* pr = partials + (size_t)row * NP;
   float M = -INFINITY;
-  for (int t = lane; t < NT; t += 32) M = fmaxf(M, pr[t].x);
+  for (int t = lane; t < NP; t += 32) M = fmaxf(M, pr[t].x);
   M = warp_max(M);
   float S = 0.f, Z = 0.f;
-  for (int t = lane; t < NT; t += 32) {
+  for (int t = lane; t < NP; t += 32) {
     const float2 q = pr[t];
     S += q.y * exp2f(q.x - M);
-    if (zsum) Z += zsum[(size_t)row * NT + t];
+    if (zsum) Z += zsum[(size_t)row * NP + t];
   }
   S = warp_sum(S);
   if (zsum) Z = warp_sum(Z);
@@ -564,10 +624,9 @@ __global__ void __launch_bounds__(kCeWarps * 32)
 // stored exponentials, in place: fp16 E -> bf16 G = kap E 2^(m_t - L2) - targets,
 // rounded once.  The label's entry is formed from its fp32 logit: q_y - 1 would
 // lose what E's rounding cuts off where the row is confident.  One block per
-// row: 8 warps, a warp at a time on a tile of 256 columns (16 bytes a lane).
-// Bound by HBM: 4 bytes per entry.
+// row, 16 bytes a thread.  Bound by HBM: 4 bytes per entry.
 __global__ void __launch_bounds__(256)
-    k_ce_dlogits(const float2* __restrict__ partials, const float* __restrict__ zsum, int NT,
+    k_ce_dlogits(const float2* __restrict__ partials, const float* __restrict__ zsum, int NP,
                  RowCount rc, int V, long long Vp, float invT, float smooth, float zloss,
                  const int32_t* __restrict__ list, const int* __restrict__ lab,
                  const float* __restrict__ zlab, const float* __restrict__ kw,
@@ -586,15 +645,15 @@ __global__ void __launch_bounds__(256)
     }
     return;
   }
-  const float2* pr = partials + (size_t)row * NT;
+  const float2* pr = partials + (size_t)row * NP;
   float M = -INFINITY, S = 0.f, Z = 0.f;
-  for (int t = threadIdx.x; t < NT; t += 256) {
+  for (int t = threadIdx.x; t < NP; t += 256) {
     const float2 q = pr[t];
     const float nm = fmaxf(M, q.x);
     const float ref = nm == -INFINITY ? 0.f : nm;
     S = S * exp2f(M - ref) + q.y * exp2f(q.x - ref);
     M = nm;
-    if (zsum) Z += zsum[(size_t)row * NT + t];
+    if (zsum) Z += zsum[(size_t)row * NP + t];
   }
   const float Mw = warp_max(M);
   S = warp_sum(S * exp2f(M - (Mw == -INFINITY ? 0.f : Mw)));
@@ -626,10 +685,8 @@ __global__ void __launch_bounds__(256)
   const float g_y = fmaf(kap, exp2f(fmaf(zlab[row], invT * kLog2e, -L2)), -(label_mass + base_mass));
   uint4* dr = dlog + (size_t)row * (Vp / 8);
 #pragma unroll 4
-  for (int t = warp; t < NT; t += 8) {
-    const int col = t * BN + lane * 8;
-    if (col >= Vp) continue;
-    const float f = kap * ex2_approx(pr[t].x - L2);
+  for (int col = (warp * 32 + lane) * 8; col < Vp; col += 8 * BN) {
+    const float f = kap * ex2_approx(pr[col >> 7].x - L2);
     uint4 q = dr[col / 8];
     float v[8];
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};

@@ -45,6 +45,7 @@ __device__ __forceinline__ void tmem_ld32_conv(uint32_t taddr, float (&v)[32]) {
 // form the student entropy H(q) = ln2 * (LSE2 - U / S) (student-entropy pass).
 template <bool kGather, bool kEntropy>
 struct EpiLseT {
+  static constexpr int kEpiWarps = 4;
   static constexpr uint32_t kSmemBytes = 0;
   static constexpr bool kUsesMapC = false;
   struct Params {
@@ -139,6 +140,7 @@ __device__ __forceinline__ void stage_release() {
 }
 
 struct EpiDlogits {
+  static constexpr int kEpiWarps = 4;
   static constexpr uint32_t kSmemBytes = 4 * 2 * 4096;
   static constexpr bool kUsesMapC = true;  // map C: dlogits [rows, V] bf16, box {64, 32}
   struct Params {
@@ -292,6 +294,7 @@ __device__ __forceinline__ void reduce_slice_to_rows(const uint8_t* buf, int lan
 }
 
 struct EpiDH {
+  static constexpr int kEpiWarps = 4;
   static constexpr uint32_t kSmemBytes = 4 * 2 * 4096;
   static constexpr bool kUsesMapC = true;  // map C: dH chunk rows [rows, H] fp32, box {32, 32}
   struct Params {
@@ -346,6 +349,7 @@ struct EpiDH {
 };
 
 struct EpiDW {
+  static constexpr int kEpiWarps = 4;
   static constexpr uint32_t kSmemBytes = 4 * 2 * 4096;
   static constexpr bool kUsesMapC = true;  // map C: dW [V, H] fp32, box {32, 32}
   struct Params {

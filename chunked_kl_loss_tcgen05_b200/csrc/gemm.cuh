@@ -20,6 +20,8 @@
 //               multicast tcgen05.commit.
 //   warps 2-5   epilogue: tcgen05.ld (thread = row), kernel-specific epilogue,
 //               then release the accumulator on the even CTA's barrier.
+//               An epilogue may use eight warps (Epi::kEpiWarps = 8, 320 threads):
+//               warps 2-5 then take columns [0, 128) of the tile, 6-9 the rest.
 // Double-buffered accumulators overlap the epilogue of one tile with the main
 // loop of the next.  Every wait is bounded (see ptx.cuh).
 //
@@ -48,12 +50,16 @@ constexpr uint32_t A_HALF_BYTES = CM * BK * 2;        // 16 KB
 constexpr uint32_t B_HALF_BYTES = (BN / 2) * BK * 2;  // 16 KB
 constexpr uint32_t PSTAGE_BYTES = A_HALF_BYTES + B_HALF_BYTES;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int GEMM_THREADS = 192;
+constexpr int GEMM_THREADS = 192;  // with four epilogue warps
 constexpr size_t SMEM_LIMIT = 232448;  // opt-in dynamic shared memory per CTA on sm_100
 
 // Dynamic shared memory: 1 KB alignment slack, the operand stages, the
-// epilogue's staging area (Epi::kSmemBytes, split over the 4 epilogue warps)
+// epilogue's staging area (Epi::kSmemBytes, split over the epilogue warps)
 // and 256 bytes of barriers.  As many stages as fit.
+template <class Epi>
+__host__ __device__ constexpr int gemm_threads() {
+  return 64 + 32 * Epi::kEpiWarps;
+}
 template <class Epi>
 __host__ __device__ constexpr int pair_stages() {
   return (int)((SMEM_LIMIT - 1024 - 256 - Epi::kSmemBytes) / PSTAGE_BYTES);
@@ -90,6 +96,7 @@ struct Work {
   int rev;       // 1: walk the k-blocks from kb1 - 1 down to kb0
   int ks;        // k segment of the unit (SCHED_SPLIT_K; 0 otherwise)
   int m0, n0;    // this CTA's first row (mt*256 + 128*rank) and the first column
+  int half;      // which 128 columns of the tile (eight epilogue warps; 0 otherwise)
   int rows;      // rows of the launch (row-tiled kernels: rows >= rows are padding)
 };
 
@@ -230,7 +237,7 @@ struct CtlArgs {
 };
 
 template <class Epi, bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * Epi::kEpiWarps, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const typename Epi::Params ep,
@@ -284,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&tfull[a]), 1);
-      mbar_init(smem_u32(&tempty[a]), 8);  // 4 epilogue warps in each CTA of the pair
+      mbar_init(smem_u32(&tempty[a]), 2 * Epi::kEpiWarps);  // epilogue warps of both CTAs
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0u;
@@ -430,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     uint32_t acc_phase = 0;
     if (sa.early) pdl_wait();  // the epilogue reads and writes what earlier kernels produce
     typename Epi::State st;
-    Epi::init(ep, st, sEpi + quarter * (Epi::kSmemBytes / 4), lane);
+    Epi::init(ep, st, sEpi + (warp - 2) * (Epi::kSmemBytes / Epi::kEpiWarps), lane);
     while (sch.next(w)) {
       bool ok = true;
       // A tile's main loop lasts tens of microseconds: the epilogue polls its
@@ -442,6 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
       tc_fence_after();
       w.m0 = w.mt * PM + (int)rank * CM;
       w.n0 = w.nt * BN;
+      w.half = (warp - 2) >> 2;
       const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN);
       Epi::tile(ep, st, w, taddr, r, &tmC, quarter, lane);
       tc_fence_before();
