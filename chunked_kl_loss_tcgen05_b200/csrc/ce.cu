@@ -1,6 +1,7 @@
 // Host side of the vocabulary cross entropy: checks, workspace layout and the
 // chunk loop.  Per chunk of C kept rows, on the caller's stream:
-//   gather rows -> logits GEMM (log-sum-exp epilogue) -> merge (row losses),
+//   gather rows -> logits GEMM (log-sum-exp epilogue) -> merge (row losses; the
+//   last block adds up the loss),
 // with gradients
 //   gather rows -> logits GEMM (and its exponentials) -> merge and dlogits, or,
 //   for given log-sum-exps, gather rows -> logits GEMM (dlogits epilogue),
@@ -15,6 +16,12 @@
 using namespace fckl;
 
 namespace {
+
+// Sleep of an epilogue between polls, per k-block of its unit.  A k-block takes
+// a pair about 280 ns, so this is a tenth of the main loop: 2 us regardless of
+// it, as long loops can afford, cost
+// 1531 x 1024 x 50257 (a step) 476 us against 417.
+constexpr int kPollNs = 30;
 
 // Room for the k segments of a chunk's dH GEMM: four units for every CTA pair
 // of a B200 (more would mean more slabs to sum than waves to balance), 256 KB
@@ -148,7 +155,6 @@ template <class Label>
 fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* dev) {
   const fckl_ce_problem* prob = q.prob;
   const bool grads = q.mode != CeMode::kFwd;
-  const bool losses = q.mode != CeMode::kBwd;
   const bool bf16_grads = prob->grad_type == FCKL_GRAD_BFLOAT;
   const int H = (int)prob->H, V = (int)prob->V;
   const long long N = prob->N;
@@ -177,8 +183,11 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
   const int narrow_h = (H % BN != 0 && H % BN <= 128) ? 1 : 0;
   const bool smooth = prob->label_smoothing > 0.f;
 
-  // Rows by label.  One block takes up to 8192 rows (8 passes of 4096 would
-  // cost more than the second launch and the memset it saves).
+  // Rows by label.  Few rows of one chunk are selected and gathered at once (a
+  // block a row, each reading all labels: up to 1024 of them cost less than a
+  // launch); else one block selects up to 8192 rows (more passes of 4096 rows
+  // would cost more than the second launch and the memset they save).
+  const bool at_once = N <= 1024 && L.nchunks == 1;
   {
     const int denom = q.mode == CeMode::kBwd || prob->reduction == FCKL_REDUCE_SUM
                           ? 1 : (int)prob->n_valid_total;
@@ -187,13 +196,25 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
                   : std::max<long long>(4096, cdiv(cdiv(N, kCompactBlocks), 4096) * 4096);
     const int nb = (int)cdiv(N, R);
     ProfScope ps(K_COUNT, st, 0.0, (double)N * (sizeof(Label) * (nb > 1 ? 2 : 1) + 4));
-    if (nb > 1) {
-      if (cudaMemsetAsync(ctl, 0, sizeof(DeviceCtl), st) != cudaSuccess) return FCKL_ERR_CUDA;
-      FCKL_LAUNCH(k_ce_count<Label>, nb, 1024, 0, labels, N, R, (long long)prob->ignore_index, V,
-                  ctl);
+    if (at_once) {
+      FCKL_LAUNCH(k_ce_select<Label>, N, 128, 0, labels, (int)N, (long long)prob->ignore_index, V,
+                  denom, list, ctl, H, static_cast<const __nv_bfloat16*>(q.hidden), q.factor,
+                  q.lse_in, hst, lab, kw, lse2);
+    } else {
+      if (nb > 1) {
+        if (cudaMemsetAsync(ctl, 0, sizeof(DeviceCtl), st) != cudaSuccess) return FCKL_ERR_CUDA;
+        FCKL_LAUNCH(k_ce_count<Label>, nb, 1024, 0, labels, N, R, (long long)prob->ignore_index, V,
+                    ctl);
+      }
+      FCKL_LAUNCH(k_ce_list<Label>, nb, 1024, 0, labels, N, R, (long long)prob->ignore_index, V,
+                  denom, list, ctl);
     }
-    FCKL_LAUNCH(k_ce_list<Label>, nb, 1024, 0, labels, N, R, (long long)prob->ignore_index, V,
-                denom, list, ctl);
+  }
+  // Blocks of the row kernels that leave loss shares, over all chunks.
+  unsigned blocks = 0;
+  for (long long c = 0; c < L.nchunks; ++c) {
+    const long long cap = std::min(L.C, N - c * L.C);
+    blocks += (unsigned)(q.mode == CeMode::kFwd ? cdiv(cap, kCeWarps) : cap);
   }
 
   CUtensorMap mapW_k, mapW_mn, mapdW, mapSlab;
@@ -225,7 +246,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     const RowCount rc{-1, ctl, (int)row0, cap};
     const double nr = (double)cap, flops = 2.0 * nr * V * H;
     const long long MT = cdiv(cap, PM);
-    {
+    if (!at_once) {
       ProfScope ps(K_GATHER, st, 0.0, nr * (H * 4.0 + 16.0));
       FCKL_LAUNCH(k_ce_gather<Label>, cap, 128, 0, clist, rc, H,
                   static_cast<const __nv_bfloat16*>(q.hidden), labels, q.factor, q.lse_in, hst, lab,
@@ -238,6 +259,8 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     if (!make_map(&mapH_k, hst, H, (long long)align_up(cap, CM), (long long)H * 2, BK, CM))
       return FCKL_ERR_CUDA;
     SchedArgs sa_v{SCHED_VOCAB_MAJOR, NT, KBh, 1, 0, rc, 0, 0};
+    sa_v.poll_ns = kPollNs;
+    sa_v.fresh_rows = at_once ? 1 : 0;
     const int Gv = grid_for(MT * NT);
     CUtensorMap mapD_st, mapD_k, mapD_mn, mapH_mn;
     if (grads && !make_map(&mapD_st, dlog, L.Vp, cap, L.Vp * 2, 64, 32)) return FCKL_ERR_CUDA;
@@ -260,7 +283,8 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       ProfScope ps(K_MERGE, st, 0.0, nr * (NT * 8.0 + 28.0));
       FCKL_LAUNCH(k_ce_merge, (int)cdiv(cap, kCeWarps), kCeWarps * 32, 0, (const float2*)part, zs,
                   NP, rc, cap, V, invT, prob->label_smoothing, prob->z_loss, clist,
-                  (const float*)zlab, (const float*)kw, q.row_loss, q.lse_out, share + row0);
+                  (const float*)zlab, (const float*)kw, q.row_loss, q.lse_out, share + row0,
+                  (const float*)share, N, ctl, blocks, q.loss);
       continue;
     }
     if (q.mode == CeMode::kFwdBwd) {
@@ -278,7 +302,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       FCKL_LAUNCH(k_ce_dlogits, cap, 256, 0, (const float2*)part, zs, NP, rc, V, L.Vp, invT,
                   prob->label_smoothing, prob->z_loss, clist, (const int*)lab, (const float*)zlab,
                   (const float*)kw, reinterpret_cast<uint4*>(dlog), q.row_loss, q.lse_out,
-                  share + row0);
+                  share + row0, (const float*)share, N, ctl, blocks, q.loss);
     } else {
       EpiCeDlogits::Params pb{V, scale2, prob->label_smoothing, 2.f * prob->z_loss, lab, kw, lse2,
                               cap};
@@ -289,7 +313,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     if (q.dH) {
       if (!make_map(&mapD_k, dlog, V, cap, L.Vp * 2, BK, CM)) return FCKL_ERR_CUDA;
       SchedArgs sa_h{SCHED_SPLIT_K, NTh, KBv, 0, 0, rc, 0, w3d, 0, narrow_h, 0, 2, 1,
-                     L.slab_units};
+                     L.slab_units, kPollNs};
       EpiCeDH::Params ph{H, invT, ctl};
       ProfScope ps(K_DH, st, flops, 2.0 * nr * V + 2.0 * (double)V * H + 4.0 * nr * H);
       FCKL_LAUNCH((gemm_pair_kernel<EpiCeDH, false, true>), 2 * pairs, gemm_threads<EpiCeDH>(),
@@ -304,6 +328,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       if (!make_map_mn(&mapH_mn, hst, H, cap, (long long)H * 2, &h3d)) return FCKL_ERR_CUDA;
       const int MTv = (int)cdiv(V, PM);
       SchedArgs sa_w{SCHED_TILES, NTh, 0, 1, MTv, rc, d3d, h3d, 0, narrow_h, q.dH ? 1 : 0};
+      sa_w.poll_ns = kPollNs;
       ProfScope ps(K_DW, st, flops,
                    2.0 * nr * (V + H) + (dw_direct16 ? 2.0 : c > 0 ? 8.0 : 4.0) * V * H);
       if (dw_direct16) {
@@ -338,10 +363,6 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     ProfScope ps(K_DW_OUT, st, 0.0, n4 * 24.0);
     FCKL_LAUNCH(k_ce_dw_out, (int)std::min<long long>(cdiv(n4, 256), (long long)dev->sms * 8), 256,
                 0, (const float4*)dw_dst, n4, static_cast<uint2*>(q.dW), (const DeviceCtl*)ctl);
-  }
-  if (losses) {
-    ProfScope ps(K_FINAL, st, 0.0, (double)N * 4.0);
-    FCKL_LAUNCH(k_ce_finalize, 1, 1024, 0, (const float*)share, N, (const DeviceCtl*)ctl, q.loss);
   }
   return cudaGetLastError() == cudaSuccess ? FCKL_OK : FCKL_ERR_CUDA;
 }

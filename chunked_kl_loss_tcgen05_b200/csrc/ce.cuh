@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(1024) k_ce_list(const Label* __restrict__ labe
     if (alone) {
       ctl->err = any_bad ? kErrBadIndex : 0u;
       ctl->timeout_site = 0u;
+      ctl->ticket = 0u;
     }
     ctl->n_rows = n;
     ctl->n_valid = denom > 0 ? denom : n;
@@ -149,6 +150,62 @@ __global__ void __launch_bounds__(128)
     kw[i] = factor ? factor[r] : 1.f;
     if (lse) lse2[i] = lse[r] * kLog2e;
   }
+}
+
+// Selection and gathering in one launch, for calls of one chunk and few rows:
+// block r counts the kept labels before its row, and all of them, by itself
+// (N labels a block), so that row r's place in the list and in hst is known.
+template <class Label>
+__global__ void __launch_bounds__(128)
+    k_ce_select(const Label* __restrict__ labels, int N, long long ignore, int V, int denom,
+                int32_t* __restrict__ list, DeviceCtl* ctl, int H,
+                const __nv_bfloat16* __restrict__ hidden, const float* __restrict__ factor,
+                const float* __restrict__ lse, __nv_bfloat16* __restrict__ hst,
+                int* __restrict__ lab, float* __restrict__ kw, float* __restrict__ lse2) {
+  __shared__ int red[2][4];
+  pdl_wait();
+  pdl_trigger();
+  const int r = blockIdx.x;
+  int before = 0, n = 0;
+  bool bad = false;
+  for (int i = threadIdx.x; i < N; i += 128) {
+    const int k = ce_keep(labels, i, ignore, V, bad) ? 1 : 0;
+    n += k;
+    before += i < r ? k : 0;
+  }
+  before = warp_sum_int(before);
+  n = warp_sum_int(n);
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = before;
+    red[1][threadIdx.x >> 5] = n;
+  }
+  bad = __syncthreads_or(bad) != 0;
+  before = red[0][0] + red[0][1] + red[0][2] + red[0][3];
+  n = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+  const long long y = (long long)labels[r];
+  bool unused = false;
+  const bool keep = ce_keep(labels, r, ignore, V, unused);
+  const int i = keep ? before : N - 1 - (r - before);
+  if (threadIdx.x == 0) {
+    list[i] = r;
+    if (keep) {
+      lab[i] = (int)y;
+      kw[i] = factor ? factor[r] : 1.f;
+      if (lse) lse2[i] = lse[r] * kLog2e;
+    }
+    if (r == 0) {
+      ctl->err = bad ? kErrBadIndex : 0u;
+      ctl->timeout_site = 0u;
+      ctl->ticket = 0u;
+      ctl->n_rows = n;
+      ctl->n_valid = denom > 0 ? denom : n;
+    }
+  }
+  if (i >= n + 64) return;
+  uint4* dst = reinterpret_cast<uint4*>(hst + (size_t)i * H);
+  const uint4* src = reinterpret_cast<const uint4*>(hidden + (size_t)r * H);
+  for (int j = threadIdx.x; j < H / 8; j += 128)
+    dst[j] = keep ? src[j] : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ---------------------------------------------------------------- epilogues
@@ -200,8 +257,13 @@ __device__ __forceinline__ float exp32(float (&v)[32], float scale2, float ref, 
 
 __device__ __forceinline__ float sum32(const float (&v)[32], int cols) {
   float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (cols >= 32) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) s[j & 3] += j < cols ? v[j] : 0.f;
+    for (int j = 0; j < 32; ++j) s[j & 3] += v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j & 3] += j < cols ? v[j] : 0.f;
+  }
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
@@ -571,6 +633,33 @@ struct EpiCeDW {
 };
 
 // ---------------------------------------------------------------- row kernels
+// loss = sum of the rows' shares / D, by whichever block of the call's row
+// kernels finishes last (ctl->ticket counts them to `blocks`), in fp64 and in
+// an order that does not depend on which it is.  Called by all 256 threads.
+__device__ __forceinline__ void ce_finish_loss(const float* share, long long N, DeviceCtl* ctl,
+                                               unsigned blocks, float* loss) {
+  __shared__ double red[8];
+  __shared__ bool s_last;
+  __threadfence();  // this block's shares before its ticket
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(&ctl->ticket, 1u) + 1u == blocks;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double s = 0.0;
+#pragma unroll 8
+  for (long long i = threadIdx.x; i < N; i += 256) s += (double)__ldcg(share + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) s += red[w];
+    const int n = ctl->n_valid;
+    *loss = ctl->n_rows > 0 && n > 0 ? (float)(s / (double)n) : 0.f;
+  }
+}
+
 // Merges the tile partials of each row into its LSE and row loss.  All rows of
 // the chunk's part of the list write the caller's row loss and LSE (0 for
 // left-out rows) and their share k_r l_r of the loss (list order).  One warp
@@ -580,44 +669,43 @@ __global__ void __launch_bounds__(kCeWarps * 32)
                RowCount rc, int cap, int V, float invT, float smooth, float zloss,
                const int32_t* __restrict__ list, const float* __restrict__ zlab,
                const float* __restrict__ kw, float* __restrict__ row_loss,
-               float* __restrict__ lse_out, float* __restrict__ share) {
+               float* __restrict__ lse_out, float* __restrict__ share,
+               const float* __restrict__ all_shares, long long N, DeviceCtl* ctl, unsigned blocks,
+               float* __restrict__ loss) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kCeWarps + (threadIdx.x >> 5);
-  if (row >= cap) return;
-  const int r = list[row];
-  if (row >= rc.get()) {
-    if (lane == 0) {
-      if (row_loss) row_loss[r] = 0.f;
-      if (lse_out) lse_out[r] = 0.f;
-      share[row] = 0.f;
+  if (row < cap) {
+    float l = 0.f, lse = 0.f, part = 0.f;
+    if (row < rc.get()) {
+      const float2* pr = partials + (size_t)row * NP;
+      float M = -INFINITY;
+      for (int t = lane; t < NP; t += 32) M = fmaxf(M, pr[t].x);
+      M = warp_max(M);
+      float S = 0.f, Z = 0.f;
+      for (int t = lane; t < NP; t += 32) {
+        const float2 q = pr[t];
+        S += q.y * exp2f(q.x - M);
+        if (zsum) Z += zsum[(size_t)row * NP + t];
+      }
+      S = warp_sum(S);
+      if (zsum) Z = warp_sum(Z);
+      lse = (M + log2f(S)) * kLn2;
+      const float nll = lse - zlab[row] * invT;
+      l = nll;
+      if (smooth > 0.f) l += smooth * ((lse - Z / (float)V * invT) - nll);
+      l = fmaf(zloss * lse, lse, l);
+      part = kw[row] * l;
     }
-    return;
+    if (lane == 0) {
+      const int r = list[row];
+      if (row_loss) row_loss[r] = l;
+      if (lse_out) lse_out[r] = lse;
+      share[row] = part;
+    }
   }
-  const float2* pr = partials + (size_t)row * NP;
-  float M = -INFINITY;
-  for (int t = lane; t < NP; t += 32) M = fmaxf(M, pr[t].x);
-  M = warp_max(M);
-  float S = 0.f, Z = 0.f;
-  for (int t = lane; t < NP; t += 32) {
-    const float2 q = pr[t];
-    S += q.y * exp2f(q.x - M);
-    if (zsum) Z += zsum[(size_t)row * NP + t];
-  }
-  S = warp_sum(S);
-  if (zsum) Z = warp_sum(Z);
-  if (lane == 0) {
-    const float L2 = M + log2f(S);
-    const float lse = L2 * kLn2;
-    const float nll = lse - zlab[row] * invT;
-    float l = nll;
-    if (smooth > 0.f) l += smooth * ((lse - Z / (float)V * invT) - nll);
-    l = fmaf(zloss * lse, lse, l);
-    if (row_loss) row_loss[r] = l;
-    if (lse_out) lse_out[r] = lse;
-    share[row] = kw[row] * l;
-  }
+  ce_finish_loss(all_shares, N, ctl, blocks, loss);
 }
 
 // Merge of EpiCeStore's partials, as k_ce_merge, and the row's dlogits from the
@@ -631,7 +719,9 @@ __global__ void __launch_bounds__(256)
                  const int32_t* __restrict__ list, const int* __restrict__ lab,
                  const float* __restrict__ zlab, const float* __restrict__ kw,
                  uint4* __restrict__ dlog, float* __restrict__ row_loss,
-                 float* __restrict__ lse_out, float* __restrict__ share) {
+                 float* __restrict__ lse_out, float* __restrict__ share,
+                 const float* __restrict__ all_shares, long long N, DeviceCtl* ctl,
+                 unsigned blocks, float* __restrict__ loss) {
   __shared__ float red[3][8];
   pdl_wait();
   pdl_trigger();
@@ -643,6 +733,7 @@ __global__ void __launch_bounds__(256)
       if (lse_out) lse_out[r] = 0.f;
       share[row] = 0.f;
     }
+    ce_finish_loss(all_shares, N, ctl, blocks, loss);
     return;
   }
   const float2* pr = partials + (size_t)row * NP;
@@ -707,26 +798,7 @@ __global__ void __launch_bounds__(256)
     dr[col / 8] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
-}
-
-// loss = sum of the rows' shares / D, fp64 in a fixed order.
-__global__ void __launch_bounds__(1024) k_ce_finalize(const float* __restrict__ share, long long N,
-                                                      const DeviceCtl* ctl, float* loss) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ double red[1024];
-  double s = 0.0;
-  for (long long i = threadIdx.x; i < N; i += blockDim.x) s += (double)share[i];
-  red[threadIdx.x] = s;
-  __syncthreads();
-  for (int w = blockDim.x >> 1; w > 0; w >>= 1) {
-    if ((int)threadIdx.x < w) red[threadIdx.x] += red[threadIdx.x + w];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    const int n = ctl->n_valid;
-    *loss = ctl->n_rows > 0 && n > 0 ? (float)(red[0] / (double)n) : 0.f;
-  }
+  ce_finish_loss(all_shares, N, ctl, blocks, loss);
 }
 
 // dH rows of one chunk: the sum of the row's slabs, in segment order, to the

@@ -142,6 +142,14 @@ struct SchedArgs {
   // SCHED_SPLIT_K with S = 0, when every k segment is stored to a slab of its
   // own: at most this many units (0: the partial tiles are added in place).
   int slab_units;
+  // How long the epilogue sleeps between two looks at its accumulator-ready
+  // barrier: 0 = 2 us (main loops of tens of microseconds), > 0 = this many ns
+  // per k-block of the unit, at most 2 us.
+  int poll_ns;
+  // 1: the kernel just ahead writes the row count itself, so every thread waits
+  // for it before the count is first read (needs early = 0).  Otherwise the
+  // count is older: complete when the kernel ahead let this one launch.
+  int fresh_rows;
 };
 
 __device__ __forceinline__ bool narrow_unit(const SchedArgs& a, const Work& w) {
@@ -259,6 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * Epi::kEpiW
   uint32_t* abort_flag = tmem_slot + 1;
   int* split_slot = reinterpret_cast<int*>(abort_flag + 1);
 
+  if (sa.fresh_rows) pdl_wait();
   // A launch over no rows (a chunk past the last compacted row) has no work:
   // both CTAs of every pair see the same count and leave before setting up
   // barriers or TMEM (still waiting for the kernel ahead, so that completion
@@ -443,7 +452,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * Epi::kEpiW
       // A tile's main loop lasts tens of microseconds: the epilogue polls its
       // accumulator-ready barrier every 2 us (measured ~0.5-0.9% faster steps
       // under the power cap than polling back to back).
-      if (lane == 0) ok = wait_phase(smem_u32(&tfull[acc]), acc_phase, wc, SITE_EPI_TFULL, 2000);
+      const uint32_t sleep_ns =
+          sa.poll_ns > 0 ? (uint32_t)min(2000, sa.poll_ns * (w.kb1 - w.kb0)) : 2000u;
+      if (lane == 0) ok = wait_phase(smem_u32(&tfull[acc]), acc_phase, wc, SITE_EPI_TFULL, sleep_ns);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
       tc_fence_after();

@@ -23,7 +23,8 @@ struct DeviceCtl {
   uint32_t timeout_site;  // which wait gave up first (diagnostics)
   int32_t n_rows;     // rows a masked call compacted (its local valid rows)
   int32_t block_count[kCompactBlocks];  // valid rows per compaction block
-  uint32_t pad[60 - kCompactBlocks];
+  uint32_t ticket;    // blocks of the row kernels that have left their loss shares
+  uint32_t pad[59 - kCompactBlocks];
 };
 static_assert(sizeof(DeviceCtl) == 256, "control block is 256 bytes");
 

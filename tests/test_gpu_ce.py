@@ -227,6 +227,27 @@ def test_bad_labels_are_reported_and_left_out(bad):
     check_grads(c, o, dH, dW)
 
 
+@pytest.mark.parametrize("N", [1, 300, 1024, 1025])
+def test_row_count_of_an_earlier_call_is_never_used(N):
+    """Calls with different counts in turn on one workspace, whose control block
+    then holds the other call's count (or, poisoned, nothing sensible) while the
+    next call's kernels start early."""
+    a, b = Case(N, 64, 700, ignored=0.0), Case(N, 64, 700, seed=1, ignored=0.5)
+    prob = FcklCeProblem(N, 64, 700)
+    ws = torch.full((fckl_ce_workspace_bytes(prob, True),), 127, dtype=torch.uint8, device="cuda")
+    refs = [(c, c.oracle(row_grad=c.g), c.oracle()) for c in (a, b)]
+    for turn in range(6):
+        c, og, o = refs[turn % 2]
+        _, rows, lse = fused_ce_fwd(c.hidden, c.W, c.labels, workspace=ws)
+        check_losses(c, o, None, rows, lse)
+        if turn >= 4:
+            ws.fill_(127)
+        check_grads(c, og, *fused_ce_bwd(c.hidden, c.W, c.labels, lse, c.row_grad, workspace=ws))
+        loss, rows, dH, dW = fused_ce_fwd_bwd(c.hidden, c.W, c.labels, workspace=ws)
+        check_losses(c, o, loss, rows)
+        check_grads(c, o, dH, dW)
+
+
 def test_ignore_index_inside_the_vocabulary():
     c = Case(200, 64, 300, ignored=0.0)
     c.labels[::3] = 7
