@@ -299,7 +299,10 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
         }
       }
       ProfScope ps(K_CE_SCALE, st, 0.0, nr * (V * 4.0 + NT * 16.0));
-      FCKL_LAUNCH(k_ce_dlogits, cap, 256, 0, (const float2*)part, zs, NP, rc, V, L.Vp, invT,
+      // blocks that share a row, so that few rows still fill the SMs
+      const unsigned parts = (unsigned)std::max<long long>(
+          1, std::min<long long>(cdiv(L.Vp, 2048), cdiv(4ll * dev->sms, cap)));
+      FCKL_LAUNCH(k_ce_dlogits, dim3(cap, parts), 256, 0, (const float2*)part, zs, NP, rc, V, L.Vp, invT,
                   prob->label_smoothing, prob->z_loss, clist, (const int*)lab, (const float*)zlab,
                   (const float*)kw, reinterpret_cast<uint4*>(dlog), q.row_loss, q.lse_out,
                   share + row0, (const float*)share, N, ctl, blocks, q.loss);
@@ -349,11 +352,11 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       const long long vecs = (long long)V * H * (bf16_grads ? 2 : 4) / 16;
       ProfScope ps(K_DH_OUT, st, 0.0, nr * H * (bf16_grads ? 6.0 : 8.0));
       if (bf16_grads)
-        FCKL_LAUNCH(k_ce_dh_out<__nv_bfloat16>, cap, 128, 0, (const float*)slab, clist, rc, H, NTh,
+        FCKL_LAUNCH(k_ce_dh_out<__nv_bfloat16>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H, NTh,
                     KBv, pairs, L.slab_units, static_cast<__nv_bfloat16*>(q.dH), zdw, vecs,
                     (const DeviceCtl*)ctl);
       else
-        FCKL_LAUNCH(k_ce_dh_out<float>, cap, 128, 0, (const float*)slab, clist, rc, H, NTh, KBv,
+        FCKL_LAUNCH(k_ce_dh_out<float>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H, NTh, KBv,
                     pairs, L.slab_units, static_cast<float*>(q.dH), zdw, vecs,
                     (const DeviceCtl*)ctl);
     }

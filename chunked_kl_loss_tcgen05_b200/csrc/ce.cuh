@@ -711,8 +711,9 @@ __global__ void __launch_bounds__(kCeWarps * 32)
 // Merge of EpiCeStore's partials, as k_ce_merge, and the row's dlogits from the
 // stored exponentials, in place: fp16 E -> bf16 G = kap E 2^(m_t - L2) - targets,
 // rounded once.  The label's entry is formed from its fp32 logit: q_y - 1 would
-// lose what E's rounding cuts off where the row is confident.  One block per
-// row, 16 bytes a thread.  Bound by HBM: 4 bytes per entry.
+// lose what E's rounding cuts off where the row is confident.  gridDim.y blocks
+// share a row (each merges its partials for itself), 16 bytes a thread at a
+// time.  Bound by HBM: 4 bytes per entry.
 __global__ void __launch_bounds__(256)
     k_ce_dlogits(const float2* __restrict__ partials, const float* __restrict__ zsum, int NP,
                  RowCount rc, int V, long long Vp, float invT, float smooth, float zloss,
@@ -726,14 +727,15 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool first = blockIdx.y == 0;  // the row's block that writes its outputs
   const int r = list[row];
   if (row >= rc.get()) {
-    if (threadIdx.x == 0) {
+    if (first && threadIdx.x == 0) {
       if (row_loss) row_loss[r] = 0.f;
       if (lse_out) lse_out[r] = 0.f;
       share[row] = 0.f;
     }
-    ce_finish_loss(all_shares, N, ctl, blocks, loss);
+    if (first) ce_finish_loss(all_shares, N, ctl, blocks, loss);
     return;
   }
   const float2* pr = partials + (size_t)row * NP;
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(256)
     Z += red[2][k];
   }
   const float L2 = M + log2f(S), lse = L2 * kLn2, k0 = kw[row], a_y = zlab[row] * invT;
-  if (threadIdx.x == 0) {
+  if (first && threadIdx.x == 0) {
     const float nll = lse - a_y;
     float l = nll;
     if (smooth > 0.f) l += smooth * ((lse - Z / (float)V * invT) - nll);
@@ -776,7 +778,8 @@ __global__ void __launch_bounds__(256)
   const float g_y = fmaf(kap, exp2f(fmaf(zlab[row], invT * kLog2e, -L2)), -(label_mass + base_mass));
   uint4* dr = dlog + (size_t)row * (Vp / 8);
 #pragma unroll 4
-  for (int col = (warp * 32 + lane) * 8; col < Vp; col += 8 * BN) {
+  for (long long col = ((long long)blockIdx.y * 256 + threadIdx.x) * 8; col < Vp;
+       col += 8 * 256 * (long long)gridDim.y) {
     const float f = kap * ex2_approx(pr[col >> 7].x - L2);
     uint4 q = dr[col / 8];
     float v[8];
@@ -787,9 +790,10 @@ __global__ void __launch_bounds__(256)
       v[2 * j] = fmaf(f, e.x, -base_mass);
       v[2 * j + 1] = fmaf(f, e.y, -base_mass);
     }
-    if ((unsigned)(y - col) < 8u) {
+    const int at = y - (int)col;
+    if ((unsigned)at < 8u) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j == y - col ? g_y : v[j];
+      for (int j = 0; j < 8; ++j) v[j] = j == at ? g_y : v[j];
     }
     if (col + 8 > V) {
 #pragma unroll
@@ -798,12 +802,12 @@ __global__ void __launch_bounds__(256)
     dr[col / 8] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
-  ce_finish_loss(all_shares, N, ctl, blocks, loss);
+  if (first) ce_finish_loss(all_shares, N, ctl, blocks, loss);
 }
 
 // dH rows of one chunk: the sum of the row's slabs, in segment order, to the
-// caller's row (zeros for left-out rows), rounded once.  One block per list
-// entry.  The number of segments is the one the dH GEMM chose (same inputs).
+// caller's row (zeros for left-out rows), rounded once.  A block takes 512
+// columns (blockIdx.y) of a list entry (blockIdx.x).  The number of segments is the one the dH GEMM chose (same inputs).
 // When the whole call kept no row, no dW launch wrote anything: the blocks zero
 // the dw_bytes of dW (dw != nullptr) instead.
 template <class Out>
@@ -816,27 +820,28 @@ __global__ void __launch_bounds__(128)
   const int i = blockIdx.x;
   const int n = rc.get();
   if (dw != nullptr && ctl->n_rows == 0)
-    for (long long j = i * (long long)blockDim.x + threadIdx.x; j < dw_vecs;
-         j += (long long)gridDim.x * blockDim.x)
+    for (long long j = ((long long)blockIdx.y * gridDim.x + i) * blockDim.x + threadIdx.x;
+         j < dw_vecs; j += (long long)gridDim.x * gridDim.y * blockDim.x)
       dw[j] = make_uint4(0u, 0u, 0u, 0u);
   if (dH == nullptr) return;
+  const int j = blockIdx.y * 512 + threadIdx.x * 4;
   Out* dst = dH + (size_t)list[i] * H;
   if (i >= n) {
-    for (int j = threadIdx.x * 4; j < H; j += blockDim.x * 4) store4(dst + j, make_float4(0, 0, 0, 0));
+    if (j < H) store4(dst + j, make_float4(0, 0, 0, 0));
     return;
   }
   const int MT = (n + PM - 1) / PM;
   const int S = choose_split_warp(MT * NTh, KB, slots, slab_units);
   const size_t pitch = (size_t)MT * PM * H;
-  const float* src = slabs + (size_t)i * H;
-  for (int j = threadIdx.x * 4; j < H; j += blockDim.x * 4) {
-    float4 a = *reinterpret_cast<const float4*>(src + j);
-    for (int s = 1; s < S; ++s) {
-      const float4 b = *reinterpret_cast<const float4*>(src + s * pitch + j);
-      a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
-    }
-    store4(dst + j, a);
+  if (j >= H) return;
+  const float* src = slabs + (size_t)i * H + j;
+  float4 a = *reinterpret_cast<const float4*>(src);
+#pragma unroll 4
+  for (int s = 1; s < S; ++s) {
+    const float4 b = *reinterpret_cast<const float4*>(src + s * pitch);
+    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
   }
+  store4(dst + j, a);
 }
 
 // bf16 dW of a call of several chunks: the fp32 sum over the chunks, rounded once.

@@ -128,10 +128,10 @@ inline bool pdl_enabled() {
 // called pdl_trigger() (or exited); it calls pdl_wait() before it touches what
 // that kernel produces.  Kernels with compile-time cluster dimensions keep them.
 template <typename... KArgs, typename... Args>
-cudaError_t launch(bool pdl, void (*kernel)(KArgs...), int grid, int block, size_t smem,
+cudaError_t launch(bool pdl, void (*kernel)(KArgs...), dim3 grid, int block, size_t smem,
                    cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -146,7 +146,7 @@ cudaError_t launch(bool pdl, void (*kernel)(KArgs...), int grid, int block, size
 // Ends the enclosing call with FCKL_ERR_CUDA when the launch fails.
 #define FCKL_LAUNCH(kernel, grid, block, smem, ...)                                          \
   do {                                                                                       \
-    if (::fckl::launch(pdl, kernel, (int)(grid), (int)(block), (size_t)(smem), st, __VA_ARGS__) != \
+    if (::fckl::launch(pdl, kernel, dim3(grid), (int)(block), (size_t)(smem), st, __VA_ARGS__) != \
         cudaSuccess)                                                                         \
       return FCKL_ERR_CUDA;                                                                  \
   } while (0)

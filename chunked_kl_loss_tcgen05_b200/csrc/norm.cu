@@ -228,20 +228,8 @@ fckl_status fckl_block_norm_bwd(const fckl_norm_problem* prob, const void* x, co
   }
   if (dpost_weight || dgate || dpre_weight) {
     ProfScope ps(K_NORM_SUM, st, 0.0, 8.0 * grid * prob->H);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)cdiv(prob->H, 64), 2, 1);
-    cfg.blockDim = dim3(512, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg,
-                           prob->weight_type == FCKL_BFLOAT ? k_norm_sum<__nv_bfloat16>
-                                                            : k_norm_sum<float>,
-                           (const NormArgs)a, grid) != cudaSuccess)
-      return FCKL_ERR_CUDA;
+    FCKL_LAUNCH(prob->weight_type == FCKL_BFLOAT ? k_norm_sum<__nv_bfloat16> : k_norm_sum<float>,
+                dim3((unsigned)cdiv(prob->H, 64), 2), 512, 0, (const NormArgs)a, grid);
   }
   return FCKL_OK;
 }
