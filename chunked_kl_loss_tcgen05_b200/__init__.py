@@ -86,9 +86,8 @@ class FcklCeProblem(ctypes.Structure):
     def __init__(self, N, H, V, T=1.0, label_smoothing=0.0, z_loss=0.0,
                  reduction=FCKL_REDUCE_MEAN, ignore_index=-100, chunk=0, n_valid_total=0,
                  label_type=FCKL_LABELS_LONG, grad_type=FCKL_GRAD_FLOAT):
-        super().__init__(int(N), int(H), int(V), float(T), float(label_smoothing), float(z_loss),
-                         int(reduction), int(ignore_index), int(chunk), int(n_valid_total),
-                         int(label_type), int(grad_type))
+        super().__init__(N, H, V, T, label_smoothing, z_loss, reduction, ignore_index, chunk,
+                         n_valid_total, label_type, grad_type)
 
 
 class FcklNormProblem(ctypes.Structure):
@@ -101,8 +100,7 @@ class FcklNormProblem(ctypes.Structure):
     def __init__(self, N, H, scale=1.0, eps=1e-6, weight_offset=0.0,
                  flags=FCKL_NORM_POST | FCKL_NORM_PRE, x_type=FCKL_BFLOAT,
                  weight_type=FCKL_BFLOAT, dy_type=FCKL_BFLOAT):
-        super().__init__(int(N), int(H), float(scale), float(eps), float(weight_offset),
-                         int(flags), int(x_type), int(weight_type), int(dy_type))
+        super().__init__(N, H, scale, eps, weight_offset, flags, x_type, weight_type, dy_type)
 
 
 class FcklKernelStat(ctypes.Structure):
@@ -282,27 +280,27 @@ def fckl_fwd_bwd_rows(prob, hidden, W, topk_idx, topk_logit, rows, n_rows, loss,
 
 
 def fckl_ce_workspace_bytes(prob: FcklCeProblem, gradients) -> int:
-    return int(load().fckl_ce_workspace_bytes(ctypes.byref(prob), 1 if gradients else 0))
+    return int((_LIB or load()).fckl_ce_workspace_bytes(prob, 1 if gradients else 0))
 
 
 def fckl_ce_fwd(prob, hidden, W, labels, row_weight, loss, row_loss, lse, workspace,
                 workspace_bytes, stream) -> int:
     """Array arguments are device addresses (ints) or None; returns the status."""
-    return load().fckl_ce_fwd(ctypes.byref(prob), hidden, W, labels, row_weight, loss, row_loss,
+    return (_LIB or load()).fckl_ce_fwd(prob, hidden, W, labels, row_weight, loss, row_loss,
                               lse, workspace, workspace_bytes, stream)
 
 
 def fckl_ce_fwd_bwd(prob, hidden, W, labels, row_weight, loss, row_loss, lse, dH, dW, workspace,
                     workspace_bytes, stream) -> int:
     """Array arguments are device addresses (ints) or None; returns the status."""
-    return load().fckl_ce_fwd_bwd(ctypes.byref(prob), hidden, W, labels, row_weight, loss,
+    return (_LIB or load()).fckl_ce_fwd_bwd(prob, hidden, W, labels, row_weight, loss,
                                   row_loss, lse, dH, dW, workspace, workspace_bytes, stream)
 
 
 def fckl_ce_bwd(prob, hidden, W, labels, lse, row_grad, dH, dW, workspace, workspace_bytes,
                 stream) -> int:
     """Array arguments are device addresses (ints) or None; returns the status."""
-    return load().fckl_ce_bwd(ctypes.byref(prob), hidden, W, labels, lse, row_grad, dH, dW,
+    return (_LIB or load()).fckl_ce_bwd(prob, hidden, W, labels, lse, row_grad, dH, dW,
                               workspace, workspace_bytes, stream)
 
 
@@ -312,12 +310,12 @@ def fckl_scale_gradient(grad, n, grad_type, factor, stream) -> int:
 
 
 def fckl_block_norm_workspace_bytes(prob: FcklNormProblem) -> int:
-    return int(load().fckl_block_norm_workspace_bytes(ctypes.byref(prob)))
+    return int((_LIB or load()).fckl_block_norm_workspace_bytes(prob))
 
 
 def fckl_block_norm_fwd(prob, x, block, post_weight, gate, pre_weight, v, y, stream) -> int:
     """Array arguments are device addresses (ints) or None; returns the status."""
-    return load().fckl_block_norm_fwd(ctypes.byref(prob), x, block, post_weight, gate, pre_weight,
+    return (_LIB or load()).fckl_block_norm_fwd(prob, x, block, post_weight, gate, pre_weight,
                                       v, y, stream)
 
 
@@ -325,7 +323,7 @@ def fckl_block_norm_bwd(prob, x, block, post_weight, gate, pre_weight, dy, dv, d
                         dpost_weight, dgate, dpre_weight, workspace, workspace_bytes,
                         stream) -> int:
     """Array arguments are device addresses (ints) or None; returns the status."""
-    return load().fckl_block_norm_bwd(ctypes.byref(prob), x, block, post_weight, gate, pre_weight,
+    return (_LIB or load()).fckl_block_norm_bwd(prob, x, block, post_weight, gate, pre_weight,
                                       dy, dv, dx, dblock, dpost_weight, dgate, dpre_weight,
                                       workspace, workspace_bytes, stream)
 
@@ -341,7 +339,8 @@ def fckl_status_string(status: int) -> str:
 KERNEL_KINDS = ("count_valid", "prep_teacher", "fwd_logits_lse", "merge_loss", "bwd_dlogits",
                 "dH_gemm", "dW_gemm", "finalize", "entropy_gemm", "merge_entropy", "gather_rows",
                 "scatter_rows", "select_rows", "zero_dw", "ce_logits", "ce_dlogits", "dH_rows",
-                "dW_round", "norm_fwd", "norm_bwd", "norm_sum", "ce_scale")
+                "dW_round", "norm_fwd", "norm_bwd", "norm_sum", "ce_scale",
+                "dH_dW_gemm")
 
 
 def fckl_profile_begin(kinds=None) -> None:

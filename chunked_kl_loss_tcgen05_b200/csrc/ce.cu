@@ -23,6 +23,14 @@ namespace {
 // 1531 x 1024 x 50257 (a step) 476 us against 417.
 constexpr int kPollNs = 30;
 
+// Calls of up to this many rows run their dH GEMM (which reads W) and their dW
+// GEMM (which writes as much) side by side, on 3/8 and 5/8 of the CTA pairs: both
+// wait for memory most of the time.  Graph-timed steps, us, one after the other
+// and side by side: 1 x 1024 x 32000 75 and 66, 128 x 4096 x 128256 757 and 706,
+// 200 x 2048 x 32000 142 and 130, 256 x 256 x 4096 33.4 and 30.7; from 256 rows
+// on (256 x 4096 x 128256: 846 and 855) the tensor cores start to limit both.
+constexpr int kTwoRows = 256;
+
 // Room for the k segments of a chunk's dH GEMM: four units for every CTA pair
 // of a B200 (more would mean more slabs to sum than waves to balance), 256 KB
 // each, or one segment of every tile.
@@ -116,6 +124,14 @@ struct CeRequest {
   void* stream = nullptr;
 };
 
+template <class E2>
+bool allow_smem_two() {
+  return cudaFuncSetAttribute(gemm_two_kernel<EpiCeDH, false, true, E2, true, true>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)std::max(pair_smem_bytes<EpiCeDH>(), pair_smem_bytes<E2>())) ==
+         cudaSuccess;
+}
+
 template <class Epi, bool A_MN, bool B_MN>
 bool allow_smem() {
   return cudaFuncSetAttribute(gemm_pair_kernel<Epi, A_MN, B_MN>,
@@ -146,7 +162,8 @@ const CeDevice* ce_device() {
            allow_smem<EpiCeStore<false>, false, false>() &&
            allow_smem<EpiCeStore<true>, false, false>() && allow_smem<EpiCeDlogits, false, false>() &&
            allow_smem<EpiCeDH, false, true>() && allow_smem<EpiCeDW, true, true>() &&
-           allow_smem<EpiCeDWSum, true, true>();
+           allow_smem<EpiCeDWSum, true, true>() && allow_smem_two<EpiCeDW>() &&
+           allow_smem_two<EpiCeDWSum>();
   }
   return &d;
 }
@@ -313,36 +330,56 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       FCKL_CE_GEMM(EpiCeDlogits, mapD_st, pb);
     }
 #undef FCKL_CE_GEMM
-    if (q.dH) {
-      if (!make_map(&mapD_k, dlog, V, cap, L.Vp * 2, BK, CM)) return FCKL_ERR_CUDA;
-      SchedArgs sa_h{SCHED_SPLIT_K, NTh, KBv, 0, 0, rc, 0, w3d, 0, narrow_h, 0, 2, 1,
-                     L.slab_units, kPollNs};
-      EpiCeDH::Params ph{H, invT, ctl};
-      ProfScope ps(K_DH, st, flops, 2.0 * nr * V + 2.0 * (double)V * H + 4.0 * nr * H);
-      FCKL_LAUNCH((gemm_pair_kernel<EpiCeDH, false, true>), 2 * pairs, gemm_threads<EpiCeDH>(),
-                  pair_smem_bytes<EpiCeDH>(), mapD_k, mapW_mn, mapSlab, ph, sa_h, ca);
-    }
-    // dW (+)= dlogits^T h: dlogits and the gathered rows were complete before
-    // the dH GEMM launched, so its main loop starts at once (without a dH GEMM
-    // it follows the recompute GEMM directly).
-    if (q.dW) {
-      int d3d = 0, h3d = 0;
-      if (!make_map_mn(&mapD_mn, dlog, L.Vp, cap, L.Vp * 2, &d3d)) return FCKL_ERR_CUDA;
-      if (!make_map_mn(&mapH_mn, hst, H, cap, (long long)H * 2, &h3d)) return FCKL_ERR_CUDA;
-      const int MTv = (int)cdiv(V, PM);
-      SchedArgs sa_w{SCHED_TILES, NTh, 0, 1, MTv, rc, d3d, h3d, 0, narrow_h, q.dH ? 1 : 0};
-      sa_w.poll_ns = kPollNs;
-      ProfScope ps(K_DW, st, flops,
-                   2.0 * nr * (V + H) + (dw_direct16 ? 2.0 : c > 0 ? 8.0 : 4.0) * V * H);
-      if (dw_direct16) {
-        EpiCeDW::Params pw{V, H, invT, ctl};
-        FCKL_LAUNCH((gemm_pair_kernel<EpiCeDW, true, true>), grid_for((long long)MTv * NTh),
-                    gemm_threads<EpiCeDW>(), pair_smem_bytes<EpiCeDW>(), mapD_mn, mapH_mn, mapdW, pw, sa_w,
-                    ca);
-      } else {
-        EpiCeDWSum::Params pw{V, H, invT, c > 0 ? 1 : 0, ctl};
-        FCKL_LAUNCH((gemm_pair_kernel<EpiCeDWSum, true, true>), grid_for((long long)MTv * NTh),
-                    gemm_threads<EpiCeDWSum>(), pair_smem_bytes<EpiCeDWSum>(), mapD_mn, mapH_mn, mapdW, pw, sa_w, ca);
+    // dH = dlogits W / (T D), k segments to slabs; dW (+)= dlogits^T h / (T D).
+    SchedArgs sa_h{SCHED_SPLIT_K, NTh, KBv, 0, 0, rc, 0, w3d, 0, narrow_h, 0, 2, 1,
+                   L.slab_units, kPollNs};
+    const EpiCeDH::Params ph{H, invT, ctl};
+    if (q.dH && !make_map(&mapD_k, dlog, V, cap, L.Vp * 2, BK, CM)) return FCKL_ERR_CUDA;
+    const int MTv = (int)cdiv(V, PM);
+    int d3d = 0, h3d = 0;
+    if (q.dW && (!make_map_mn(&mapD_mn, dlog, L.Vp, cap, L.Vp * 2, &d3d) ||
+                 !make_map_mn(&mapH_mn, hst, H, cap, (long long)H * 2, &h3d)))
+      return FCKL_ERR_CUDA;
+    SchedArgs sa_w{SCHED_TILES, NTh, 0, 1, MTv, rc, d3d, h3d, 0, narrow_h, 0};
+    sa_w.poll_ns = kPollNs;
+    const EpiCeDW::Params pw{V, H, invT, ctl};
+    const EpiCeDWSum::Params ps_w{V, H, invT, c > 0 ? 1 : 0, ctl};
+    const double dh_bytes = 2.0 * nr * V + 2.0 * (double)V * H + 4.0 * nr * H;
+    const double dw_bytes = 2.0 * nr * (V + H) + (dw_direct16 ? 2.0 : c > 0 ? 8.0 : 4.0) * V * H;
+    const bool two = q.dH && q.dW && L.nchunks == 1 && cap <= kTwoRows;
+    const int dh_pairs = two ? std::max(1, pairs * 3 / 8) : pairs;
+    if (two) {
+      ProfScope ps(K_DHW, st, 2.0 * flops, dh_bytes + dw_bytes);
+      constexpr size_t smem =
+          std::max({pair_smem_bytes<EpiCeDH>(), pair_smem_bytes<EpiCeDW>(), pair_smem_bytes<EpiCeDWSum>()});
+      if (dw_direct16)
+        FCKL_LAUNCH((gemm_two_kernel<EpiCeDH, false, true, EpiCeDW, true, true>), 2 * pairs,
+                    gemm_threads<EpiCeDH>(), smem, mapD_k, mapW_mn, mapSlab, mapD_mn, mapH_mn,
+                    mapdW, ph, pw, sa_h, sa_w, ca, dh_pairs);
+      else
+        FCKL_LAUNCH((gemm_two_kernel<EpiCeDH, false, true, EpiCeDWSum, true, true>), 2 * pairs,
+                    gemm_threads<EpiCeDH>(), smem, mapD_k, mapW_mn, mapSlab, mapD_mn, mapH_mn,
+                    mapdW, ph, ps_w, sa_h, sa_w, ca, dh_pairs);
+    } else {
+      if (q.dH) {
+        ProfScope ps(K_DH, st, flops, dh_bytes);
+        FCKL_LAUNCH((gemm_pair_kernel<EpiCeDH, false, true>), 2 * pairs, gemm_threads<EpiCeDH>(),
+                    pair_smem_bytes<EpiCeDH>(), mapD_k, mapW_mn, mapSlab, ph, sa_h, ca);
+      }
+      if (q.dW) {
+        // dlogits and the gathered rows were complete before the dH GEMM
+        // launched, so this main loop starts at once (without a dH GEMM it
+        // follows the kernel that wrote dlogits)
+        sa_w.early = q.dH ? 1 : 0;
+        ProfScope ps(K_DW, st, flops, dw_bytes);
+        if (dw_direct16)
+          FCKL_LAUNCH((gemm_pair_kernel<EpiCeDW, true, true>), grid_for((long long)MTv * NTh),
+                      gemm_threads<EpiCeDW>(), pair_smem_bytes<EpiCeDW>(), mapD_mn, mapH_mn, mapdW,
+                      pw, sa_w, ca);
+        else
+          FCKL_LAUNCH((gemm_pair_kernel<EpiCeDWSum, true, true>), grid_for((long long)MTv * NTh),
+                      gemm_threads<EpiCeDWSum>(), pair_smem_bytes<EpiCeDWSum>(), mapD_mn, mapH_mn,
+                      mapdW, ps_w, sa_w, ca);
       }
     }
     // the last chunk's blocks zero dW when no row was kept
@@ -353,11 +390,11 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       ProfScope ps(K_DH_OUT, st, 0.0, nr * H * (bf16_grads ? 6.0 : 8.0));
       if (bf16_grads)
         FCKL_LAUNCH(k_ce_dh_out<__nv_bfloat16>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H, NTh,
-                    KBv, pairs, L.slab_units, static_cast<__nv_bfloat16*>(q.dH), zdw, vecs,
+                    KBv, dh_pairs, L.slab_units, static_cast<__nv_bfloat16*>(q.dH), zdw, vecs,
                     (const DeviceCtl*)ctl);
       else
         FCKL_LAUNCH(k_ce_dh_out<float>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H, NTh, KBv,
-                    pairs, L.slab_units, static_cast<float*>(q.dH), zdw, vecs,
+                    dh_pairs, L.slab_units, static_cast<float*>(q.dH), zdw, vecs,
                     (const DeviceCtl*)ctl);
     }
   }

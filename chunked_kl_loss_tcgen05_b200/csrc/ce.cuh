@@ -777,30 +777,44 @@ __global__ void __launch_bounds__(256)
   const int y = lab[row];
   const float g_y = fmaf(kap, exp2f(fmaf(zlab[row], invT * kLog2e, -L2)), -(label_mass + base_mass));
   uint4* dr = dlog + (size_t)row * (Vp / 8);
-#pragma unroll 4
-  for (long long col = ((long long)blockIdx.y * 256 + threadIdx.x) * 8; col < Vp;
-       col += 8 * 256 * (long long)gridDim.y) {
-    const float f = kap * ex2_approx(pr[col >> 7].x - L2);
-    uint4 q = dr[col / 8];
-    float v[8];
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  const long long vecs = Vp / 8, step = 256ll * gridDim.y;
+  constexpr int kAhead = 4;  // loads in flight per thread
+  for (long long i0 = 256ll * blockIdx.y + threadIdx.x; i0 < vecs; i0 += kAhead * step) {
+    uint4 q[kAhead];
+    float m[kAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-      v[2 * j] = fmaf(f, e.x, -base_mass);
-      v[2 * j + 1] = fmaf(f, e.y, -base_mass);
+    for (int u = 0; u < kAhead; ++u) {
+      const long long i = i0 + u * step;
+      if (i < vecs) {
+        q[u] = dr[i];
+        m[u] = pr[i >> 4].x;  // 16 vectors to a half tile
+      }
     }
-    const int at = y - (int)col;
-    if ((unsigned)at < 8u) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j == at ? g_y : v[j];
-    }
-    if (col + 8 > V) {
+    for (int u = 0; u < kAhead; ++u) {
+      const long long i = i0 + u * step;
+      if (i >= vecs) break;
+      const float f = kap * ex2_approx(m[u] - L2);
+      const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+      float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = col + j < V ? v[j] : 0.f;
+      for (int j = 0; j < 4; ++j) {
+        const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        v[2 * j] = fmaf(f, e.x, -base_mass);
+        v[2 * j + 1] = fmaf(f, e.y, -base_mass);
+      }
+      const int at = y - 8 * (int)i;
+      if ((unsigned)at < 8u) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j == at ? g_y : v[j];
+      }
+      if (8 * i + 8 > V) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 8 * i + j < V ? v[j] : 0.f;
+      }
+      dr[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                         pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }
-    dr[col / 8] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
   if (first) ce_finish_loss(all_shares, N, ctl, blocks, loss);
 }

@@ -244,12 +244,14 @@ struct CtlArgs {
   int debug_skip_commit;  // >0: the MMA thread omits its first accumulator-ready commit
 };
 
+// One GEMM on the calling CTA's pair, number `cluster` of the `nclusters` that
+// share its units.  The tensor maps are kernel parameters.
 template <class Epi, bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * Epi::kEpiWarps, 1)
-    gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
-                     const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmC, const typename Epi::Params ep,
-                     const SchedArgs sa, const CtlArgs ca) {
+__device__ __forceinline__ void gemm_pair_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                               const CUtensorMap& tmC,
+                                               const typename Epi::Params& ep, const SchedArgs& sa,
+                                               const CtlArgs& ca, const int cluster,
+                                               const int nclusters) {
   constexpr int STAGES = pair_stages<Epi>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -281,8 +283,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * Epi::kEpiW
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int cluster = blockIdx.x >> 1;
-  const int nclusters = gridDim.x >> 1;
 
   if (warp == 0) {
     // Split-K factor chosen here when only the device knows the rows; every
@@ -477,6 +477,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * Epi::kEpiW
   cluster_sync_all();  // neither CTA releases TMEM or exits while the pair still uses it
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+template <class Epi, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * Epi::kEpiWarps, 1)
+    gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmC, const typename Epi::Params ep,
+                     const SchedArgs sa, const CtlArgs ca) {
+  gemm_pair_body<Epi, A_MN, B_MN>(tmA, tmB, tmC, ep, sa, ca, blockIdx.x >> 1, gridDim.x >> 1);
+}
+
+// Two independent GEMMs side by side in one launch: the first `pairs1` CTA pairs
+// work on the first, the others on the second.
+template <class E1, bool A1, bool B1, class E2, bool A2, bool B2>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * E1::kEpiWarps, 1)
+    gemm_two_kernel(const __grid_constant__ CUtensorMap tmA1,
+                    const __grid_constant__ CUtensorMap tmB1,
+                    const __grid_constant__ CUtensorMap tmC1,
+                    const __grid_constant__ CUtensorMap tmA2,
+                    const __grid_constant__ CUtensorMap tmB2,
+                    const __grid_constant__ CUtensorMap tmC2, const typename E1::Params ep1,
+                    const typename E2::Params ep2, const SchedArgs sa1, const SchedArgs sa2,
+                    const CtlArgs ca, int pairs1) {
+  static_assert(E1::kEpiWarps == E2::kEpiWarps, "one block size");
+  const int cluster = blockIdx.x >> 1;
+  if (cluster < pairs1)
+    gemm_pair_body<E1, A1, B1>(tmA1, tmB1, tmC1, ep1, sa1, ca, cluster, pairs1);
+  else
+    gemm_pair_body<E2, A2, B2>(tmA2, tmB2, tmC2, ep2, sa2, ca, cluster - pairs1,
+                               (int)(gridDim.x >> 1) - pairs1);
 }
 
 }  // namespace fckl

@@ -403,6 +403,28 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The stream handle without building a torch.cuda.Stream (a call of a few
+# microseconds on the GPU would wait for it).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_device(index, call, *args):
+    """call(*args, stream) with device ``index`` current, on its current stream."""
+    if index == torch.cuda.current_device():
+        return call(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return call(*args, _raw_stream(index))
+
+
+def _placed(index, tensors):
+    """Whether every tensor (None aside) is contiguous on CUDA device ``index``."""
+    for t in tensors:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            return False
+    return index >= 0
+
+
 def _ce_setup(hidden, W, labels, rows, T, label_smoothing, z_loss, ignore_index, reduction, chunk,
               n_valid_total, grad_dtype, workspace, gradients):
     """Checks, the problem and the workspace of a cross-entropy call.  ``rows``:
@@ -415,13 +437,14 @@ def _ce_setup(hidden, W, labels, rows, T, label_smoothing, z_loss, ignore_index,
     if labels.dim() != 1 or labels.shape[0] != N:
         raise ValueError(f"labels must be [N={N}], got {tuple(labels.shape)}")
     for name, t in rows:
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (N,)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (N,)):
             raise TypeError(f"{name} must be a float32 tensor [N={N}]")
     if reduction not in _REDUCTIONS:
         raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}, got {reduction!r}")
     if grad_dtype not in _GRAD_TYPES:
         raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
-    _check_placement(True, [("hidden", hidden), ("W", W), ("labels", labels)] + list(rows))
+    if not _placed(hidden.get_device(), (hidden, W, labels) + tuple(t for _, t in rows)):
+        _check_placement(True, [("hidden", hidden), ("W", W), ("labels", labels)] + list(rows))
     prob = FcklCeProblem(N, H, W.shape[0], T, label_smoothing, z_loss, _REDUCTIONS[reduction],
                          ignore_index, chunk, n_valid_total, _LABEL_TYPES[labels.dtype],
                          _GRAD_TYPES[grad_dtype])
@@ -443,9 +466,10 @@ def _check_grad_out(name, t, shape, dtype, device):
         raise ValueError(f"out {name} must be a contiguous {dtype} tensor {shape} on {device}")
 
 
-def _finish(status, where, workspace, stream, check):
+def _finish(status, where, workspace, check):
     if status == FCKL_OK and check:
-        where, status = "fckl_check", fckl_check(workspace.data_ptr(), stream)
+        where = "fckl_check"
+        status = _on_device(workspace.get_device(), fckl_check, workspace.data_ptr())
     if status != FCKL_OK:
         raise FcklError(status, where)
 
@@ -465,12 +489,10 @@ def fused_ce_fwd(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0,
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     row_loss = torch.empty(prob.N, dtype=torch.float32, device=dev)
     lse = torch.empty(prob.N, dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = fckl_ce_fwd(prob, hidden.data_ptr(), W.data_ptr(), labels.data_ptr(),
-                         _ptr(row_weight), loss.data_ptr(), row_loss.data_ptr(), lse.data_ptr(),
-                         workspace.data_ptr(), workspace.numel(), stream)
-        _finish(st, "fckl_ce_fwd", workspace, stream, check)
+    st = _on_device(dev.index, fckl_ce_fwd, prob, hidden.data_ptr(), W.data_ptr(),
+                    labels.data_ptr(), _ptr(row_weight), loss.data_ptr(), row_loss.data_ptr(),
+                    lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _finish(st, "fckl_ce_fwd", workspace, check)
     return loss, row_loss, lse
 
 
@@ -494,12 +516,10 @@ def _fused_ce_fwd_bwd(hidden, W, labels, row_weight, T, label_smoothing, z_loss,
         dW = torch.empty(prob.V, prob.H, dtype=grad_dtype, device=dev) if want[1] else None
     row_loss = torch.empty(prob.N, dtype=torch.float32, device=dev)
     lse = torch.empty(prob.N, dtype=torch.float32, device=dev) if want_lse else None
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = fckl_ce_fwd_bwd(prob, hidden.data_ptr(), W.data_ptr(), labels.data_ptr(),
-                             _ptr(row_weight), loss.data_ptr(), row_loss.data_ptr(), _ptr(lse),
-                             _ptr(dH), _ptr(dW), workspace.data_ptr(), workspace.numel(), stream)
-        _finish(st, "fckl_ce_fwd_bwd", workspace, stream, check)
+    st = _on_device(dev.index, fckl_ce_fwd_bwd, prob, hidden.data_ptr(), W.data_ptr(),
+                    labels.data_ptr(), _ptr(row_weight), loss.data_ptr(), row_loss.data_ptr(),
+                    _ptr(lse), _ptr(dH), _ptr(dW), workspace.data_ptr(), workspace.numel())
+    _finish(st, "fckl_ce_fwd_bwd", workspace, check)
     return loss, row_loss, lse, dH, dW
 
 
@@ -539,12 +559,10 @@ def fused_ce_bwd(hidden, W, labels, lse, row_grad, T=1.0, label_smoothing=0.0, z
     else:
         dH = torch.empty(prob.N, prob.H, dtype=grad_dtype, device=dev) if want[0] else None
         dW = torch.empty(prob.V, prob.H, dtype=grad_dtype, device=dev) if want[1] else None
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = fckl_ce_bwd(prob, hidden.data_ptr(), W.data_ptr(), labels.data_ptr(), lse.data_ptr(),
-                         row_grad.data_ptr(), _ptr(dH), _ptr(dW), workspace.data_ptr(),
-                         workspace.numel(), stream)
-        _finish(st, "fckl_ce_bwd", workspace, stream, check)
+    st = _on_device(dev.index, fckl_ce_bwd, prob, hidden.data_ptr(), W.data_ptr(),
+                    labels.data_ptr(), lse.data_ptr(), row_grad.data_ptr(), _ptr(dH), _ptr(dW),
+                    workspace.data_ptr(), workspace.numel())
+    _finish(st, "fckl_ce_bwd", workspace, check)
     return dH, dW
 
 
@@ -552,9 +570,8 @@ def _scale_gradient(t, factor):
     """t *= factor (a device float32 scalar) in place; free when the factor is 1."""
     if t is None:
         return
-    with torch.cuda.device(t.device):
-        st = fckl_scale_gradient(t.data_ptr(), t.numel(), _GRAD_TYPES[t.dtype], factor.data_ptr(),
-                                 torch.cuda.current_stream(t.device).cuda_stream)
+    st = _on_device(t.get_device(), fckl_scale_gradient, t.data_ptr(), t.numel(),
+                    _GRAD_TYPES[t.dtype], factor.data_ptr())
     if st != FCKL_OK:
         raise FcklError(st, "fckl_scale_gradient")
 
@@ -641,9 +658,8 @@ def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_sm
 _REAL_TYPES = {torch.float32: FCKL_FLOAT, torch.bfloat16: FCKL_BFLOAT}
 
 
-def _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps, weight_offset,
-                  dy=None, dv=None):
-    """Checks of a block_norm call and its problem."""
+def _norm_checks(x, block, post_weight, gate, pre_weight, dy=None, dv=None):
+    """Shapes, dtypes and placement of a block_norm call, named one by one."""
     if x.dim() != 2:
         raise ValueError(f"x must be [N,H]; got {tuple(x.shape)}")
     N, H = x.shape
@@ -667,9 +683,29 @@ def _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps
         if w.dtype not in _REAL_TYPES or w.dtype != weights[0][1].dtype:
             raise TypeError("post_weight, gate and pre_weight must all be float32 or all bfloat16")
     _check_placement(True, rows + tuple(weights))
-    flags = (FCKL_NORM_POST if post else 0) | (FCKL_NORM_PRE if pre else 0)
-    wt = _REAL_TYPES[weights[0][1].dtype] if weights else FCKL_FLOAT
-    return FcklNormProblem(N, H, scale, eps, weight_offset, flags, _REAL_TYPES[x.dtype], wt,
+
+
+def _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps, weight_offset,
+                  dy=None, dv=None):
+    """The checked problem of a block_norm call.  One quick pass over the tensors;
+    only what it does not accept goes through the checks that name the fault."""
+    shape, index, wt, ok = x.shape, x.get_device(), None, x.dim() == 2
+    if ok:
+        row = shape[1:]
+        for w in (post_weight, gate, pre_weight):
+            if w is not None:
+                wt = wt or w.dtype
+                ok = ok and w.dtype == wt and w.shape == row
+        ok = (ok and x.dtype in _REAL_TYPES and (wt is None or wt in _REAL_TYPES)
+              and (block is None or (block.shape == shape and block.dtype == torch.bfloat16))
+              and (dy is None or (dy.shape == shape and dy.dtype in _REAL_TYPES))
+              and (dv is None or (dv.shape == shape and dv.dtype == x.dtype))
+              and _placed(index, (x, block, post_weight, gate, pre_weight, dy, dv)))
+    if not ok:
+        _norm_checks(x, block, post_weight, gate, pre_weight, dy, dv)
+    return FcklNormProblem(shape[0], shape[1], scale, eps, weight_offset,
+                           (FCKL_NORM_POST if post else 0) | (FCKL_NORM_PRE if pre else 0),
+                           _REAL_TYPES[x.dtype], _REAL_TYPES[wt] if wt else FCKL_FLOAT,
                            FCKL_BFLOAT if dy is None else _REAL_TYPES[dy.dtype])
 
 
@@ -690,11 +726,9 @@ def block_norm_fwd(x, block=None, post_weight=None, gate=None, pre_weight=None, 
                          weight_offset)
     dev = x.device
     v = torch.empty_like(x) if block is not None and (want_residual or not pre) else None
-    y = torch.empty(prob.N, prob.H, dtype=torch.bfloat16, device=dev) if pre else None
-    with torch.cuda.device(dev):
-        st = fckl_block_norm_fwd(prob, x.data_ptr(), _ptr(block), _ptr(post_weight), _ptr(gate),
-                                 _ptr(pre_weight), _ptr(v), _ptr(y),
-                                 torch.cuda.current_stream(dev).cuda_stream)
+    y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if pre else None
+    st = _on_device(dev.index, fckl_block_norm_fwd, prob, x.data_ptr(), _ptr(block),
+                    _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(v), _ptr(y))
     if st != FCKL_OK:
         raise FcklError(st, "fckl_block_norm_fwd")
     return (x if block is None else v), y
@@ -730,11 +764,10 @@ def block_norm_bwd(x, block=None, dy=None, dv=None, post_weight=None, gate=None,
            for on, w in zip(want[2:], (post_weight, gate, pre_weight))]
     if dx is None and dblock is None and not any(d is not None for d in dws):
         return None, None, None, None, None
-    with torch.cuda.device(dev):
-        st = fckl_block_norm_bwd(prob, x.data_ptr(), _ptr(block), _ptr(post_weight), _ptr(gate),
-                                 _ptr(pre_weight), _ptr(dy), _ptr(dv), _ptr(dx), _ptr(dblock),
-                                 _ptr(dws[0]), _ptr(dws[1]), _ptr(dws[2]), workspace.data_ptr(),
-                                 workspace.numel(), torch.cuda.current_stream(dev).cuda_stream)
+    st = _on_device(dev.index, fckl_block_norm_bwd, prob, x.data_ptr(), _ptr(block),
+                    _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(dy), _ptr(dv), _ptr(dx),
+                    _ptr(dblock), _ptr(dws[0]), _ptr(dws[1]), _ptr(dws[2]), workspace.data_ptr(),
+                    workspace.numel())
     if st != FCKL_OK:
         raise FcklError(st, "fckl_block_norm_bwd")
     return dx, dblock, dws[0], dws[1], dws[2]

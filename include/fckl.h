@@ -459,7 +459,7 @@ const char* fckl_status_string(fckl_status status);
  *        rows write their results in place, no kernel of this kind runs),
  *        12 select_rows, 13 zero_dw, 14 ce_logits, 15 ce_dlogits, 16 dH_rows,
  *        17 dW_round, 18 norm_fwd, 19 norm_bwd, 20 norm_sum,
- *        21 ce_scale. */
+ *        21 ce_scale, 22 dH_dW_gemm. */
 typedef struct {
   char name[32];     /* kernel kind, e.g. "fwd_logits_lse" */
   int64_t launches;  /* launches recorded */
