@@ -215,8 +215,9 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     ProfScope ps(K_COUNT, st, 0.0, (double)N * (sizeof(Label) * (nb > 1 ? 2 : 1) + 4));
     if (at_once) {
       FCKL_LAUNCH(k_ce_select<Label>, N, 128, 0, labels, (int)N, (long long)prob->ignore_index, V,
-                  denom, list, ctl, H, static_cast<const __nv_bfloat16*>(q.hidden), q.factor,
-                  q.lse_in, hst, lab, kw, lse2);
+                  denom, list, ctl, H, static_cast<const __nv_bfloat16*>(q.hidden),
+                  static_cast<const __nv_bfloat16*>(q.W), q.factor, q.lse_in, hst, lab, zlab, kw,
+                  lse2);
     } else {
       if (nb > 1) {
         if (cudaMemsetAsync(ctl, 0, sizeof(DeviceCtl), st) != cudaSuccess) return FCKL_ERR_CUDA;
@@ -264,10 +265,11 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     const double nr = (double)cap, flops = 2.0 * nr * V * H;
     const long long MT = cdiv(cap, PM);
     if (!at_once) {
-      ProfScope ps(K_GATHER, st, 0.0, nr * (H * 4.0 + 16.0));
+      ProfScope ps(K_GATHER, st, 0.0, nr * (H * 6.0 + 20.0));
       FCKL_LAUNCH(k_ce_gather<Label>, cap, 128, 0, clist, rc, H,
-                  static_cast<const __nv_bfloat16*>(q.hidden), labels, q.factor, q.lse_in, hst, lab,
-                  kw, lse2);
+                  static_cast<const __nv_bfloat16*>(q.hidden),
+                  static_cast<const __nv_bfloat16*>(q.W), labels, q.factor, q.lse_in, hst, lab,
+                  zlab, kw, lse2);
     }
     CUtensorMap mapH_k;
     // whole boxes of 128 rows: a box that reaches past the map's end loads more
@@ -290,10 +292,10 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       {
         ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + nr * NT * 8.0);
         if (smooth) {
-          EpiCe<true>::Params pf{V, NP, scale2, lab, zlab, part, zsum};
+          EpiCe<true>::Params pf{V, NP, scale2, lab, part, zsum};
           FCKL_CE_GEMM(EpiCe<true>, mapW_k, pf);
         } else {
-          EpiCe<false>::Params pf{V, NP, scale2, lab, zlab, part, nullptr};
+          EpiCe<false>::Params pf{V, NP, scale2, lab, part, nullptr};
           FCKL_CE_GEMM(EpiCe<false>, mapW_k, pf);
         }
       }
@@ -308,10 +310,10 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       {
         ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
         if (smooth) {
-          EpiCeStore<true>::Params pf{V, NP, scale2, lab, zlab, part, zsum, cap};
+          EpiCeStore<true>::Params pf{V, NP, scale2, lab, part, zsum, cap};
           FCKL_CE_GEMM(EpiCeStore<true>, mapD_st, pf);
         } else {
-          EpiCeStore<false>::Params pf{V, NP, scale2, lab, zlab, part, nullptr, cap};
+          EpiCeStore<false>::Params pf{V, NP, scale2, lab, part, nullptr, cap};
           FCKL_CE_GEMM(EpiCeStore<false>, mapD_st, pf);
         }
       }
@@ -324,8 +326,8 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
                   (const float*)kw, reinterpret_cast<uint4*>(dlog), q.row_loss, q.lse_out,
                   share + row0, (const float*)share, N, ctl, blocks, q.loss);
     } else {
-      EpiCeDlogits::Params pb{V, scale2, prob->label_smoothing, 2.f * prob->z_loss, lab, kw, lse2,
-                              cap};
+      EpiCeDlogits::Params pb{V, scale2, prob->label_smoothing, 2.f * prob->z_loss, lab, kw, zlab,
+                              lse2, cap};
       ProfScope ps(K_CE_DLOGITS, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
       FCKL_CE_GEMM(EpiCeDlogits, mapD_st, pb);
     }

@@ -10,6 +10,13 @@
 // upstream gradient); 1 / (T D) is applied in the fp32 epilogues of dH and dW,
 // so that the bf16 operand G stays O(k_r).  D = the number of kept rows (mean)
 // or 1.
+//
+// The label's logit is a dot product of its own in fp32 (in the gather), and the
+// tiles' sums leave the label out.  The tensor cores cut every partial sum to
+// fp32 (256 of them at H = 4096), which costs a logit of 12 about 2e-5; in the
+// difference LSE - a_y the label would carry that error in full.  So instead
+//   nll = log(1 + R), R = sum_{v != y} exp(a_v - a_y),  q_y - 1 = -R / (1 + R),
+// which also keeps its relative accuracy where the row is confident (R small).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -119,7 +126,32 @@ __global__ void __launch_bounds__(1024) k_ce_list(const Label* __restrict__ labe
   }
 }
 
+// Copies H/8 vectors of a hidden row and returns, on thread 0, its dot product
+// with the label's row of W, both by a block of 128 threads.
+__device__ __forceinline__ float copy_and_dot(const __nv_bfloat16* __restrict__ src,
+                                              const __nv_bfloat16* __restrict__ wrow,
+                                              __nv_bfloat16* __restrict__ dst, int H) {
+  __shared__ float red[4];
+  float2 s = both(0.f);
+  for (int j = threadIdx.x; j < H / 8; j += 128) {
+    Raw8<__nv_bfloat16> a, b;
+    a.load(src + 8 * j);
+    b.load(wrow + 8 * j);
+    reinterpret_cast<uint4*>(dst)[j] = a.a;
+    float2 x[4], y[4];
+    a.get(x);
+    b.get(y);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s = fma2(x[k], y[k], s);
+  }
+  const float t = warp_sum(s.x + s.y);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
 // One chunk's kept rows, gathered: hidden row -> hst[i], label -> lab[i], the
+// label's logit -> zlab[i], the
 // row's factor (weight, upstream gradient, or 1) -> kw[i], and, when the
 // caller gives the log-sum-exps, log2(e) times them -> lse2[i].  The 64 rows
 // behind the last one get zero hidden rows: the dW GEMM reads whole blocks of
@@ -128,25 +160,27 @@ __global__ void __launch_bounds__(1024) k_ce_list(const Label* __restrict__ labe
 template <class Label>
 __global__ void __launch_bounds__(128)
     k_ce_gather(const int32_t* __restrict__ list, RowCount rc, int H,
-                const __nv_bfloat16* __restrict__ hidden, const Label* __restrict__ labels,
-                const float* __restrict__ factor, const float* __restrict__ lse,
-                __nv_bfloat16* __restrict__ hst, int* __restrict__ lab, float* __restrict__ kw,
+                const __nv_bfloat16* __restrict__ hidden, const __nv_bfloat16* __restrict__ W,
+                const Label* __restrict__ labels, const float* __restrict__ factor,
+                const float* __restrict__ lse, __nv_bfloat16* __restrict__ hst,
+                int* __restrict__ lab, float* __restrict__ zlab, float* __restrict__ kw,
                 float* __restrict__ lse2) {
   pdl_wait();
   pdl_trigger();
   const int i = blockIdx.x;
   const int n = rc.get();
   if (i >= n + 64) return;
-  uint4* dst = reinterpret_cast<uint4*>(hst + (size_t)i * H);
+  __nv_bfloat16* dst = hst + (size_t)i * H;
   if (i >= n) {
-    for (int j = threadIdx.x; j < H / 8; j += blockDim.x) dst[j] = make_uint4(0u, 0u, 0u, 0u);
+    for (int j = threadIdx.x; j < H / 8; j += 128)
+      reinterpret_cast<uint4*>(dst)[j] = make_uint4(0u, 0u, 0u, 0u);
     return;
   }
-  const int r = list[i];
-  const uint4* src = reinterpret_cast<const uint4*>(hidden + (size_t)r * H);
-  for (int j = threadIdx.x; j < H / 8; j += blockDim.x) dst[j] = src[j];
+  const int r = list[i], y = (int)labels[r];
+  const float z = copy_and_dot(hidden + (size_t)r * H, W + (size_t)y * H, dst, H);
   if (threadIdx.x == 0) {
-    lab[i] = (int)labels[r];
+    lab[i] = y;
+    zlab[i] = z;
     kw[i] = factor ? factor[r] : 1.f;
     if (lse) lse2[i] = lse[r] * kLog2e;
   }
@@ -159,9 +193,10 @@ template <class Label>
 __global__ void __launch_bounds__(128)
     k_ce_select(const Label* __restrict__ labels, int N, long long ignore, int V, int denom,
                 int32_t* __restrict__ list, DeviceCtl* ctl, int H,
-                const __nv_bfloat16* __restrict__ hidden, const float* __restrict__ factor,
-                const float* __restrict__ lse, __nv_bfloat16* __restrict__ hst,
-                int* __restrict__ lab, float* __restrict__ kw, float* __restrict__ lse2) {
+                const __nv_bfloat16* __restrict__ hidden, const __nv_bfloat16* __restrict__ W,
+                const float* __restrict__ factor, const float* __restrict__ lse,
+                __nv_bfloat16* __restrict__ hst, int* __restrict__ lab, float* __restrict__ zlab,
+                float* __restrict__ kw, float* __restrict__ lse2) {
   __shared__ int red[2][4];
   pdl_wait();
   pdl_trigger();
@@ -202,10 +237,14 @@ __global__ void __launch_bounds__(128)
     }
   }
   if (i >= n + 64) return;
-  uint4* dst = reinterpret_cast<uint4*>(hst + (size_t)i * H);
-  const uint4* src = reinterpret_cast<const uint4*>(hidden + (size_t)r * H);
-  for (int j = threadIdx.x; j < H / 8; j += 128)
-    dst[j] = keep ? src[j] : make_uint4(0u, 0u, 0u, 0u);
+  __nv_bfloat16* dst = hst + (size_t)i * H;
+  if (!keep) {
+    for (int j = threadIdx.x; j < H / 8; j += 128)
+      reinterpret_cast<uint4*>(dst)[j] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  const float z = copy_and_dot(hidden + (size_t)r * H, W + (size_t)y * H, dst, H);
+  if (threadIdx.x == 0) zlab[i] = z;
 }
 
 // ---------------------------------------------------------------- epilogues
@@ -267,11 +306,12 @@ __device__ __forceinline__ float sum32(const float (&v)[32], int cols) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-__device__ __forceinline__ float pick32(const float (&v)[32], int at) {
-  float z = 0.f;
+// The label's column out of the maximum and the sum: -inf in its place.
+__device__ __forceinline__ void leave_out(float (&v)[32], int at) {
+  if ((unsigned)at < 32u) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) z = j == at ? v[j] : z;
-  return z;
+    for (int j = 0; j < 32; ++j) v[j] = j == at ? -INFINITY : v[j];
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -279,9 +319,9 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Forward: per row and half tile, (max, sum 2^(a2 - max)) of a2 = z log2(e) / T,
-// z at the row's label if it lies in the half, and (kSum) the half's sum of z
-// for label smoothing.  The logits are not written.
+// Forward: per row and half tile, (max, sum 2^(a2 - max)) of a2 = z log2(e) / T
+// over the columns but the label, and (kSum) the half's sum of z for label
+// smoothing.  The logits are not written.
 template <bool kSum>
 struct EpiCe {
   static constexpr int kEpiWarps = 8;
@@ -291,7 +331,6 @@ struct EpiCe {
     int V, NP;
     float scale2;          // log2(e) / T
     const int* lab;        // [rows]
-    float* zlab;           // [rows] z at the label
     float2* partials;      // [rows, NP]
     float* zsum;           // [rows, NP] (kSum)
   };
@@ -301,7 +340,7 @@ struct EpiCe {
                               const CUtensorMap*, int, int) {
     const int row = w.m0 + r, n0 = w.n0 + w.half * 128;
     const bool rv = row < w.rows;
-    const int y = rv ? __ldg(p.lab + row) - n0 : -1;  // label's column in the half
+    const int y = rv ? __ldg(p.lab + row) - n0 : -1;  // the label's column in the half
     float m = -INFINITY, s = 0.f, u = 0.f;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
@@ -309,8 +348,8 @@ struct EpiCe {
       tmem_ld32_conv(taddr + (uint32_t)(w.half * 128 + c * 32), v);
       const int cols = rv ? p.V - (n0 + c * 32) : 0;
       if (cols <= 0) continue;
-      if ((y >> 5) == c) p.zlab[row] = pick32(v, y & 31);
       if (kSum) u += sum32(v, cols);
+      leave_out(v, y - 32 * c);
       const float nm = fmaxf(m, max32(v, cols) * p.scale2);
       const float ref = nm == -INFINITY ? 0.f : nm;  // a slice of -inf only adds 0, not NaN
       s = s * ex2_approx(m - ref) + exp32(v, p.scale2, ref, cols);
@@ -344,7 +383,6 @@ struct EpiCeStore {
     int V, NP;
     float scale2;
     const int* lab;
-    float* zlab;
     float2* partials;      // [rows, NP] (m, sum of E before rounding)
     float* zsum;
     int store_rows;        // rows of the store map
@@ -367,8 +405,8 @@ struct EpiCeStore {
       float v[32];
       tmem_ld32_conv(ta + (uint32_t)(c * 32), v);
       const int cols = rv ? p.V - (n0 + c * 32) : 0;
-      if ((y >> 5) == c) p.zlab[row] = pick32(v, y & 31);
       if (kSum) u += sum32(v, cols);
+      leave_out(v, y - 32 * c);
       top = fmaxf(top, max32(v, cols));
     }
     const float m = fmaf(top, p.scale2, -15.f);
@@ -387,6 +425,7 @@ struct EpiCeStore {
       for (int h = 0; h < 2; ++h) {
         float v[32];
         tmem_ld32_conv(ta + (uint32_t)(c * 64 + h * 32), v);
+        leave_out(v, y - 64 * c - 32 * h);
         s += exp32(v, p.scale2, ref, cols - 32 * h);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -413,6 +452,13 @@ struct EpiCeStore {
   }
 };
 
+// k [q_y (1 + zl) - (1 - e) - e / V] from q1 = q_y - 1, zl = 2 lam LSE and
+// base = k e / V.
+__device__ __forceinline__ float ce_label_grad(float k, float q1, float zl, float smooth,
+                                               float base) {
+  return fmaf(k, fmaf(q1, 1.f + zl, zl + smooth), -base);
+}
+
 // Backward without the forward's exponentials (the row-gradient call):
 // recomputed z tile -> G (see the top), rounded once to bf16 and TMA-stored to
 // the chunk's [rows, Vp] block.  Columns in [V, Vp) and the rows behind the last
@@ -428,6 +474,7 @@ struct EpiCeDlogits {
     float zloss2;          // 2 lam
     const int* lab;        // [rows]
     const float* kw;       // [rows] k_r
+    const float* zlab;     // [rows] z at the label
     const float* lse2;     // [rows] log2(e) LSE
     int store_rows;        // rows of the store map
   };
@@ -446,7 +493,12 @@ struct EpiCeDlogits {
     const float lse2 = rv ? p.lse2[row] : 0.f;
     const int y = rv ? p.lab[row] - n0 : -1;
     const float kap = kw * fmaf(p.zloss2, lse2 * kLn2, 1.f);
-    const float label_mass = kw * (1.f - p.smooth), base_mass = kw * p.smooth / (float)p.V;
+    const float base_mass = kw * p.smooth / (float)p.V;
+    float g_y = 0.f;  // the label's entry
+    if ((unsigned)y < 128u) {
+      const float q1 = expm1f(fmaf(p.zlab[row], p.scale2, -lse2) * kLn2);  // q_y - 1
+      g_y = ce_label_grad(kw, q1, p.zloss2 * lse2 * kLn2, p.smooth, base_mass);
+    }
     const int y0 = w.m0 + quarter * 32;
     const int y_end = min((w.rows + 63) & ~63, p.store_rows);
     const float2 sc = both(p.scale2), ml = both(-lse2), kk = both(kap), nb = both(-base_mass);
@@ -468,7 +520,7 @@ struct EpiCeDlogits {
         }
         if ((unsigned)yc < 32u) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = j == yc ? v[j] - label_mass : v[j];
+          for (int j = 0; j < 32; ++j) v[j] = j == yc ? g_y : v[j];
         }
         if (cols < 32) {
 #pragma unroll
@@ -660,6 +712,26 @@ __device__ __forceinline__ void ce_finish_loss(const float* share, long long N, 
   }
 }
 
+// A row from its merged partials over the columns but the label: S 2^M (base 2),
+// the label's exponent a2 = z_y log2(e) / T, and the mean of a_v (smoothing).
+struct CeRow {
+  float L2, lse, nll, loss, q1;  // log2(e) LSE, LSE, LSE - a_y, l_r, q_y - 1
+  __device__ __forceinline__ CeRow(float M, float S, float a2, float mean, float smooth,
+                                   float zloss) {
+    const float x = (M - a2) + log2f(S);  // log2 R; -inf when the label is alone
+    // beyond 2^24 the 1 in 1 + R is below R's last bit
+    const float R = exp2f(x);
+    nll = x > 24.f ? x * kLn2 : log1pf(R);
+    if (!(a2 < INFINITY)) nll = NAN;  // an overflowed label logit is no certainty
+    q1 = x > 24.f ? exp2f(-x) - 1.f : -R / (1.f + R);
+    lse = fmaf(a2, kLn2, nll);
+    L2 = fmaf(nll, kLog2e, a2);
+    loss = nll;
+    if (smooth > 0.f) loss += smooth * ((lse - mean) - nll);
+    loss = fmaf(zloss * lse, lse, loss);
+  }
+};
+
 // Merges the tile partials of each row into its LSE and row loss.  All rows of
 // the chunk's part of the list write the caller's row loss and LSE (0 for
 // left-out rows) and their share k_r l_r of the loss (list order).  One warp
@@ -686,16 +758,14 @@ __global__ void __launch_bounds__(kCeWarps * 32)
       float S = 0.f, Z = 0.f;
       for (int t = lane; t < NP; t += 32) {
         const float2 q = pr[t];
-        S += q.y * exp2f(q.x - M);
+        S += q.y * exp2f(q.x - (M == -INFINITY ? 0.f : M));
         if (zsum) Z += zsum[(size_t)row * NP + t];
       }
       S = warp_sum(S);
       if (zsum) Z = warp_sum(Z);
-      lse = (M + log2f(S)) * kLn2;
-      const float nll = lse - zlab[row] * invT;
-      l = nll;
-      if (smooth > 0.f) l += smooth * ((lse - Z / (float)V * invT) - nll);
-      l = fmaf(zloss * lse, lse, l);
+      const CeRow w(M, S, zlab[row] * (invT * kLog2e), Z / (float)V * invT, smooth, zloss);
+      l = w.loss;
+      lse = w.lse;
       part = kw[row] * l;
     }
     if (lane == 0) {
@@ -710,8 +780,7 @@ __global__ void __launch_bounds__(kCeWarps * 32)
 
 // Merge of EpiCeStore's partials, as k_ce_merge, and the row's dlogits from the
 // stored exponentials, in place: fp16 E -> bf16 G = kap E 2^(m_t - L2) - targets,
-// rounded once.  The label's entry is formed from its fp32 logit: q_y - 1 would
-// lose what E's rounding cuts off where the row is confident.  gridDim.y blocks
+// rounded once; the label's entry, which E leaves out, from q_y - 1.  gridDim.y blocks
 // share a row (each merges its partials for itself), 16 bytes a thread at a
 // time.  Bound by HBM: 4 bytes per entry.
 __global__ void __launch_bounds__(256)
@@ -762,20 +831,17 @@ __global__ void __launch_bounds__(256)
     S += red[1][k] * exp2f(red[0][k] - (M == -INFINITY ? 0.f : M));
     Z += red[2][k];
   }
-  const float L2 = M + log2f(S), lse = L2 * kLn2, k0 = kw[row], a_y = zlab[row] * invT;
+  const CeRow w(M, S, zlab[row] * (invT * kLog2e), Z / (float)V * invT, smooth, zloss);
+  const float L2 = w.L2, k0 = kw[row];
   if (first && threadIdx.x == 0) {
-    const float nll = lse - a_y;
-    float l = nll;
-    if (smooth > 0.f) l += smooth * ((lse - Z / (float)V * invT) - nll);
-    l = fmaf(zloss * lse, lse, l);
-    if (row_loss) row_loss[r] = l;
-    if (lse_out) lse_out[r] = lse;
-    share[row] = k0 * l;
+    if (row_loss) row_loss[r] = w.loss;
+    if (lse_out) lse_out[r] = w.lse;
+    share[row] = k0 * w.loss;
   }
-  const float kap = k0 * fmaf(2.f * zloss, lse, 1.f);
-  const float label_mass = k0 * (1.f - smooth), base_mass = k0 * smooth / (float)V;
+  const float zl = 2.f * zloss * w.lse, kap = fmaf(k0, zl, k0);
+  const float base_mass = k0 * smooth / (float)V;
   const int y = lab[row];
-  const float g_y = fmaf(kap, exp2f(fmaf(zlab[row], invT * kLog2e, -L2)), -(label_mass + base_mass));
+  const float g_y = ce_label_grad(k0, w.q1, zl, smooth, base_mass);
   uint4* dr = dlog + (size_t)row * (Vp / 8);
   const long long vecs = Vp / 8, step = 256ll * gridDim.y;
   constexpr int kAhead = 4;  // loads in flight per thread
@@ -795,11 +861,11 @@ __global__ void __launch_bounds__(256)
       const long long i = i0 + u * step;
       if (i >= vecs) break;
       const float f = kap * ex2_approx(m[u] - L2);
-      const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+      const uint32_t bits[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
       float v[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&bits[j]));
         v[2 * j] = fmaf(f, e.x, -base_mass);
         v[2 * j + 1] = fmaf(f, e.y, -base_mass);
       }
