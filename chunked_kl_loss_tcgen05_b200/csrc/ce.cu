@@ -23,6 +23,15 @@ namespace {
 // 1531 x 1024 x 50257 (a step) 476 us against 417.
 constexpr int kPollNs = 30;
 
+// The tensor cores add 16 products at a time to an fp32 accumulator and cut the
+// sum instead of rounding it, H / 16 times: the logits come out too small in
+// magnitude.  A sum that grows evenly loses (1/2)(mean of ulp(s)/s = 0.72 2^-23)
+// (k / n) of its final value at step k, 0.18 (H / 16) 2^-23 in all; measured, the
+// log-sum-exps fall short by 0.13 to 0.18 (H / 16) 2^-23 of the logits that make
+// them up, for H from 512 to 16384 and logits from 0.2 to 30 (4e-6 at H = 4096).
+// The scale that the epilogues multiply the logits with makes up for 0.14 of it.
+constexpr double kCutShare = 0.14;
+
 // Calls of up to this many rows run their dH GEMM (which reads W) and their dW
 // GEMM (which writes as much) side by side, on 3/8 and 5/8 of the CTA pairs: both
 // wait for memory most of the time.  Graph-timed steps, us, one after the other
@@ -192,7 +201,9 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
   __nv_bfloat16* hst = static_cast<__nv_bfloat16*>(at(L.off_h));
   __nv_bfloat16* dlog = static_cast<__nv_bfloat16*>(at(L.off_dlog));
   float* slab = static_cast<float*>(at(L.off_slab));
-  const float invT = 1.f / prob->T, scale2 = kLog2e / prob->T;
+  const float invT = 1.f / prob->T;
+  const float scale2 = (float)(1.4426950408889634 / prob->T *
+                               (1.0 + kCutShare * (H / 16.0) / 8388608.0));
   const CtlArgs ca{ctl, wait_timeout_ns(), 0};
   const int pairs = dev->sms / 2;
   const int NT = (int)L.NT, NTh = (int)L.NTh, NP = 2 * NT;  // log-sum-exp partials of 128 columns
@@ -326,7 +337,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
                   (const float*)kw, reinterpret_cast<uint4*>(dlog), q.row_loss, q.lse_out,
                   share + row0, (const float*)share, N, ctl, blocks, q.loss);
     } else {
-      EpiCeDlogits::Params pb{V, scale2, prob->label_smoothing, 2.f * prob->z_loss, lab, kw, zlab,
+      EpiCeDlogits::Params pb{V, scale2, invT * kLog2e, prob->label_smoothing, 2.f * prob->z_loss, lab, kw, zlab,
                               lse2, cap};
       ProfScope ps(K_CE_DLOGITS, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
       FCKL_CE_GEMM(EpiCeDlogits, mapD_st, pb);

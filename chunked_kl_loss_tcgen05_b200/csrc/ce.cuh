@@ -13,7 +13,7 @@
 //
 // The label's logit is a dot product of its own in fp32 (in the gather), and the
 // tiles' sums leave the label out.  The tensor cores cut every partial sum to
-// fp32 (256 of them at H = 4096), which costs a logit of 12 about 2e-5; in the
+// fp32 (256 of them at H = 4096), which moves a logit of 12 by up to 5e-5; in the
 // difference LSE - a_y the label would carry that error in full.  So instead
 //   nll = log(1 + R), R = sum_{v != y} exp(a_v - a_y),  q_y - 1 = -R / (1 + R),
 // which also keeps its relative accuracy where the row is confident (R small).
@@ -329,7 +329,7 @@ struct EpiCe {
   static constexpr bool kUsesMapC = false;
   struct Params {
     int V, NP;
-    float scale2;          // log2(e) / T
+    float scale2;          // log2(e) / T (and the cut sums' share)
     const int* lab;        // [rows]
     float2* partials;      // [rows, NP]
     float* zsum;           // [rows, NP] (kSum)
@@ -469,7 +469,8 @@ struct EpiCeDlogits {
   static constexpr bool kUsesMapC = true;  // map C: [rows, Vp] bf16, box {64, 32}
   struct Params {
     int V;
-    float scale2;          // log2(e) / T
+    float scale2;          // log2(e) / T (and the cut sums' share)
+    float label_scale2;    // log2(e) / T
     float smooth;          // label smoothing e
     float zloss2;          // 2 lam
     const int* lab;        // [rows]
@@ -496,7 +497,7 @@ struct EpiCeDlogits {
     const float base_mass = kw * p.smooth / (float)p.V;
     float g_y = 0.f;  // the label's entry
     if ((unsigned)y < 128u) {
-      const float q1 = expm1f(fmaf(p.zlab[row], p.scale2, -lse2) * kLn2);  // q_y - 1
+      const float q1 = expm1f(fmaf(p.zlab[row], p.label_scale2, -lse2) * kLn2);  // q_y - 1
       g_y = ce_label_grad(kw, q1, p.zloss2 * lse2 * kLn2, p.smooth, base_mass);
     }
     const int y0 = w.m0 + quarter * 32;
