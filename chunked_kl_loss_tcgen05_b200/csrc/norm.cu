@@ -42,30 +42,32 @@ int norm_sms() {
 constexpr int kSms = 148;             // of a B200: the workspace rule needs no GPU
 constexpr size_t kRingBytes = 216 << 10;  // shared memory of an SM for the rings
 
-// Launch shape.  A row takes a warp up to 512 values, else a block of as many
+// Launch shape.  A row takes 8, 16 or 32 lanes up to 64, 128 or 256 values, in
+// the forward 32 lanes with two vectors each up to 512 (46 us for 65536 rows of
+// 512; the backward would spill: 98 us, with blocks 75), else a block of as many
 // threads as it has vectors (two vectors a thread beyond 4096 values).  `per_sm`
 // blocks share an SM: 512 threads in the backward (at up to 128 registers), 1024
 // in the forward; each gets its part of the ring memory, in 2 to 4 stages.
 struct Shape {
-  bool warp_row;
+  int lanes;  // 0: a block a row
   int threads, nv, per_sm, rows_per_block;
   int padded;  // values of a row in the ring (whole threads)
 };
 Shape norm_shape(long long H, bool bwd) {
   Shape s{};
   const int nvec = (int)(H / 8);
-  s.warp_row = H <= kNormWarpH;
-  if (s.warp_row) {
+  s.lanes = H > (bwd ? 256 : 512) ? 0 : H <= 64 ? 8 : H <= 128 ? 16 : 32;
+  if (s.lanes) {
     s.nv = nvec <= 32 ? 1 : 2;
-    s.threads = kNormRowWarps * 32;
-    s.rows_per_block = kNormRowWarps;
+    s.threads = kNormLaneBlock;
+    s.rows_per_block = kNormLaneBlock / s.lanes;
   } else {
     s.nv = nvec <= 512 ? 1 : 2;
     s.threads = (int)align_up((size_t)cdiv(nvec, s.nv), 32);
     s.rows_per_block = 1;
   }
-  s.padded = (s.warp_row ? 32 : s.threads) * s.nv * 8;
-  s.per_sm = std::max(1, (bwd || (s.nv == 2 && !s.warp_row) ? 512 : 1024) / s.threads);
+  s.padded = (s.lanes ? s.lanes : s.threads) * s.nv * 8;
+  s.per_sm = std::max(1, (bwd || (s.nv == 2 && !s.lanes) ? 512 : 1024) / s.threads);
   return s;
 }
 int norm_grid(const Shape& s, long long N, int sms) {
@@ -104,13 +106,17 @@ using KernelFn = void (*)(const NormArgs);
 
 template <class XT, class WT>
 KernelFn pick_fwd(const Shape& s) {
-  if (s.warp_row) return s.nv == 1 ? k_norm_fwd<true, XT, WT, 1> : k_norm_fwd<true, XT, WT, 2>;
-  return s.nv == 1 ? k_norm_fwd<false, XT, WT, 1> : k_norm_fwd<false, XT, WT, 2>;
+  if (s.lanes == 8) return k_norm_fwd<8, XT, WT, 1>;
+  if (s.lanes == 16) return k_norm_fwd<16, XT, WT, 1>;
+  if (s.lanes == 32) return s.nv == 1 ? k_norm_fwd<32, XT, WT, 1> : k_norm_fwd<32, XT, WT, 2>;
+  return s.nv == 1 ? k_norm_fwd<0, XT, WT, 1> : k_norm_fwd<0, XT, WT, 2>;
 }
 template <class XT, class DT, class WT>
 KernelFn pick_bwd3(const Shape& s) {
-  if (s.warp_row) return s.nv == 1 ? k_norm_bwd<true, XT, DT, WT, 1> : k_norm_bwd<true, XT, DT, WT, 2>;
-  return s.nv == 1 ? k_norm_bwd<false, XT, DT, WT, 1> : k_norm_bwd<false, XT, DT, WT, 2>;
+  if (s.lanes == 8) return k_norm_bwd<8, XT, DT, WT, 1>;
+  if (s.lanes == 16) return k_norm_bwd<16, XT, DT, WT, 1>;
+  if (s.lanes == 32) return k_norm_bwd<32, XT, DT, WT, 1>;
+  return s.nv == 1 ? k_norm_bwd<0, XT, DT, WT, 1> : k_norm_bwd<0, XT, DT, WT, 2>;
 }
 template <class XT, class DT>
 KernelFn pick_bwd2(const fckl_norm_problem* p, const Shape& s) {
@@ -215,8 +221,8 @@ fckl_status fckl_block_norm_bwd(const fckl_norm_problem* prob, const void* x, co
                                               (dy ? (prob->dy_type == FCKL_BFLOAT ? 2 : 4) : 0));
   a.stages = norm_stages(s, row_bytes);
   size_t smem = a.stages * row_bytes * s.rows_per_block;
-  if (s.warp_row)  // the sums of the block's warps take its place at the end
-    smem = std::max(smem, (size_t)kNormRowWarps * 2 * prob->H * 4);
+  if (s.lanes)  // the sums of the block's rows take its place at the end
+    smem = std::max(smem, (size_t)s.rows_per_block * 2 * prob->H * 4);
   const bool pdl = pdl_enabled();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const double xs = xb ? 2.0 : 4.0, n = (double)prob->N * prob->H;

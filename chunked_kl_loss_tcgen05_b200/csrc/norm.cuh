@@ -19,8 +19,8 @@
 // db out.  Rows go through a ring of shared-memory stages filled by 16-byte
 // asynchronous copies, several rows ahead; a thread copies exactly the values
 // it will read, so the data needs no barrier, and the waits are the copies'
-// own.  A row of more than 512 values takes a block, a shorter one a warp
-// (eight rows a block).  What limits the kernels below HBM speed is latency, of
+// own.  A long row takes a block, a short one 32, 16 or 8 lanes of a warp (8, 16
+// or 32 rows a block).  What limits the kernels below HBM speed is latency, of
 // shuffles and barriers first: so all sums of a row go through one reduction,
 // which also carries the next row's sum of b^2 (the only one that has to come
 // before the others), and several values share a reduction's shuffles.
@@ -33,8 +33,7 @@
 namespace fckl {
 
 constexpr int kNormHMax = 8192;
-constexpr int kNormWarpH = 512;      // rows up to this length take one warp
-constexpr int kNormRowWarps = 8;     // rows of a block then
+constexpr int kNormLaneBlock = 256;  // threads of a block of rows shorter than a warp's reach
 
 struct NormArgs {
   long long N;
@@ -67,12 +66,13 @@ struct NormArgs {
 // alternates), so one barrier per call is enough; it starts zeroed, for the
 // warps a block does not have.
 constexpr int kNormRed = 2 * 8 * 16;
-template <bool kWarpRow, int K>
+template <int kLanes, int K>
 __device__ __forceinline__ void row_sums(float (&s)[K], float* red, int& turn) {
   static_assert(K == 2 || K == 8, "values per reduction");
+  constexpr int L = kLanes ? kLanes : 32;  // lanes that reduce by shuffles
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int n = K / 2, m = 16; n >= 1; n /= 2, m /= 2) {
+  for (int n = K / 2, m = L / 2; n >= 1; n /= 2, m /= 2) {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const bool up = lane & m;
@@ -80,11 +80,11 @@ __device__ __forceinline__ void row_sums(float (&s)[K], float* red, int& turn) {
       s[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
     }
   }
-  constexpr int kGroup = 32 / K;  // lanes that now share value lane / kGroup
+  constexpr int kGroup = L / K;  // lanes that now share value (lane % L) / kGroup
   float x = s[0];
 #pragma unroll
   for (int m = kGroup / 2; m >= 1; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
-  if constexpr (!kWarpRow) {
+  if constexpr (kLanes == 0) {
     float* r = red + (turn & 1) * (kNormRed / 2);
     ++turn;
     if (lane % kGroup == 0) r[lane / kGroup * 16 + (threadIdx.x >> 5)] = x;
@@ -101,7 +101,7 @@ __device__ __forceinline__ void row_sums(float (&s)[K], float* red, int& turn) {
     for (int m = kGroup / 2; m >= 1; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
   }
 #pragma unroll
-  for (int k = 0; k < K; ++k) s[k] = __shfl_sync(0xffffffffu, x, k * kGroup);
+  for (int k = 0; k < K; ++k) s[k] = __shfl_sync(0xffffffffu, x, (lane & ~(L - 1)) + k * kGroup);
 }
 
 // Eight weights (+ offset), or ones.
@@ -141,19 +141,23 @@ __device__ __forceinline__ void copy_wait_two(int stages) {
 }
 constexpr int kNormStagesMax = 4;
 
-// A thread's place in its row, and how the rows are dealt.
-template <bool kWarpRow>
+// A thread's place in its row, and how the rows are dealt: kLanes lanes a row, or
+// (0) a block.  The rows of one warp come and go together, so that its shuffles
+// always meet; `on` tells whether this thread's row exists.
+template <int kLanes>
 struct NormRows {
-  int tid, threads;      // within the row
-  long long r, step;
+  int tid, threads, place;  // within the row; the row's place in the block
+  long long r, step, ahead; // row, rows per round, distance to the warp's first row
   __device__ __forceinline__ NormRows() {
-    if (kWarpRow) {
-      tid = threadIdx.x & 31; threads = 32;
-      r = blockIdx.x * (long long)kNormRowWarps + (threadIdx.x >> 5);
-      step = gridDim.x * (long long)kNormRowWarps;
+    if (kLanes) {
+      constexpr int L = kLanes ? kLanes : 32;
+      tid = threadIdx.x % L; threads = L; place = threadIdx.x / L;
+      r = blockIdx.x * (long long)(kNormLaneBlock / L) + place;
+      step = gridDim.x * (long long)(kNormLaneBlock / L);
+      ahead = place % (32 / L);
     } else {
-      tid = threadIdx.x; threads = blockDim.x;
-      r = blockIdx.x; step = gridDim.x;
+      tid = threadIdx.x; threads = blockDim.x; place = 0;
+      r = blockIdx.x; step = gridDim.x; ahead = 0;
     }
   }
 };
@@ -223,23 +227,23 @@ __device__ __forceinline__ void norm_weights(const NormArgs& a, int tid, int thr
 }
 
 // NV vectors of eight per thread: columns 8 (tid + k threads).
-template <bool kWarpRow, class XT, class WT, int NV>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : NV == 1 ? 2 : 1)
+template <int kLanes, class XT, class WT, int NV>
+__global__ void __launch_bounds__(kLanes ? 256 : 512, kLanes ? 2 : NV == 1 ? 2 : 1)
     k_norm_fwd(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) float red[kNormRed];
   pdl_wait();
   pdl_trigger();
   const float invH = 1.f / (float)a.H;
-  const NormRows<kWarpRow> rows;
-  const NormRing<XT, float> g(ring, a, rows.threads * NV * 8, kWarpRow ? threadIdx.x >> 5 : 0);
+  const NormRows<kLanes> rows;
+  const NormRing<XT, float> g(ring, a, rows.threads * NV * 8, rows.place);
   float2 c[NV][4], w2[NV][4];
   norm_weights<WT, NV>(a, rows.tid, rows.threads, c, w2);
   for (int i = threadIdx.x; i < kNormRed; i += blockDim.x) red[i] = 0.f;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
     if (8 * (rows.tid + k * rows.threads) >= a.H) ring_zero(g, a, 8 * (rows.tid + k * rows.threads));
-  if constexpr (!kWarpRow) __syncthreads();
+  if constexpr (kLanes == 0) __syncthreads();
   auto fetch = [&](long long r, int stage) {
     if (r < a.N) {
       const long long o = r * a.H;
@@ -268,13 +272,14 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : NV == 1 ?
   int turn = 0, stage = 0;
   for (int i = 0; i < a.stages; ++i) fetch(rows.r + i * rows.step, i);
   float rho_b = 1.f;
-  if (a.post && rows.r < a.N) {
+  if (a.post && rows.r - rows.ahead < a.N) {
     copy_wait_two(a.stages);
     float s[2] = {square_b(0), 0.f};
-    row_sums<kWarpRow>(s, red, turn);
+    row_sums<kLanes>(s, red, turn);
     rho_b = rsqrtf(fmaf(s[0], invH, a.eps));
   }
-  for (long long r = rows.r; r < a.N; r += rows.step) {
+  for (long long r = rows.r; r - rows.ahead < a.N; r += rows.step) {
+    const bool on = r < a.N;
     copy_wait_two(a.stages);  // this row and the next one
     const uint8_t* s = g.base + stage * g.bytes;
     const long long o = r * a.H;
@@ -300,17 +305,17 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : NV == 1 ?
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int col = 8 * (rows.tid + k * rows.threads);
-        if (col < a.H) store8(static_cast<XT*>(a.v) + o + col, v[k]);
+        if (on && col < a.H) store8(static_cast<XT*>(a.v) + o + col, v[k]);
       }
     }
-    row_sums<kWarpRow>(sums, red, turn);
+    row_sums<kLanes>(sums, red, turn);
     rho_b = a.post ? rsqrtf(fmaf(sums[1], invH, a.eps)) : 1.f;
     if (!a.pre) continue;
     const float rho = rsqrtf(fmaf(sums[0], invH, a.eps));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int col = 8 * (rows.tid + k * rows.threads);
-      if (col >= a.H) continue;
+      if (!on || col >= a.H) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[k][i] = mul2(mul2(v[k][i], both(rho)), w2[k][i]);
       store8(static_cast<__nv_bfloat16*>(a.y) + o + col, v[k]);
@@ -319,16 +324,16 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : NV == 1 ?
   copy_wait<0>();
 }
 
-template <bool kWarpRow, class XT, class DT, class WT, int NV>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : 1)
+template <int kLanes, class XT, class DT, class WT, int NV>
+__global__ void __launch_bounds__(kLanes ? 256 : 512, kLanes ? 2 : 1)
     k_norm_bwd(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) float red[kNormRed];
   pdl_wait();
   pdl_trigger();
   const float invH = 1.f / (float)a.H;
-  const NormRows<kWarpRow> rows;
-  const NormRing<XT, DT> g(ring, a, rows.threads * NV * 8, kWarpRow ? threadIdx.x >> 5 : 0);
+  const NormRows<kLanes> rows;
+  const NormRing<XT, DT> g(ring, a, rows.threads * NV * 8, rows.place);
   float2 c[NV][4], w2[NV][4], P[NV][4], D[NV][4];
   norm_weights<WT, NV>(a, rows.tid, rows.threads, c, w2);
   for (int i = threadIdx.x; i < kNormRed; i += blockDim.x) red[i] = 0.f;
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : 1)
     zero8(D[k]);
     if (8 * (rows.tid + k * rows.threads) >= a.H) ring_zero(g, a, 8 * (rows.tid + k * rows.threads));
   }
-  if constexpr (!kWarpRow) __syncthreads();
+  if constexpr (kLanes == 0) __syncthreads();
   auto fetch = [&](long long r, int stage) {
     if (r < a.N) {
       const long long o = r * a.H;
@@ -369,13 +374,14 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : 1)
   int turn = 0, stage = 0;
   for (int i = 0; i < a.stages; ++i) fetch(rows.r + i * rows.step, i);
   float rho_b = 1.f;
-  if (a.post && rows.r < a.N) {
+  if (a.post && rows.r - rows.ahead < a.N) {
     copy_wait_two(a.stages);
     float s[2] = {square_b(0), 0.f};
-    row_sums<kWarpRow>(s, red, turn);
+    row_sums<kLanes>(s, red, turn);
     rho_b = rsqrtf(fmaf(s[0], invH, a.eps));
   }
-  for (long long r = rows.r; r < a.N; r += rows.step) {
+  for (long long r = rows.r; r - rows.ahead < a.N; r += rows.step) {
+    const bool on = r < a.N;
     copy_wait_two(a.stages);  // this row and the next one
     const uint8_t* s = g.base + stage * g.bytes;
     const long long o = r * a.H;
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : 1)
     float sums[8] = {qv.x + qv.y, qt.x + qt.y, q1.x + q1.y, q2.x + q2.y, q3.x + q3.y,
                      a.post && r + rows.step < a.N ? square_b(next) : 0.f, 0.f, 0.f};
     if (kKeep) fetch(r + a.stages * rows.step, stage);  // this thread's part has been read
-    row_sums<kWarpRow>(sums, red, turn);
+    row_sums<kLanes>(sums, red, turn);
     float k1 = 0.f, k2 = 0.f;
     if (a.pre) {
       k1 = rsqrtf(fmaf(sums[0], invH, a.eps));
@@ -423,6 +429,7 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : 1)
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int col = 8 * (rows.tid + k * rows.threads), h = kKeep ? k : 0;
+      if (!on) continue;  // nothing of a row that is not there goes into P and D
       if (!kKeep) load(col, n[h], dy[h], dv[h]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -443,10 +450,10 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : 1)
   copy_wait<0>();
   if (!a.dw1 && !a.dg && !a.dw2) return;
   float* p = a.part + (size_t)blockIdx.x * 2 * a.H;
-  if constexpr (kWarpRow) {  // the block's eight rows of sums become one, in warp order
+  if constexpr (kLanes > 0) {  // the block's rows of sums become one, in order
     __syncthreads();
-    float* sum = reinterpret_cast<float*>(ring);  // [8][2][H]
-    float* w = sum + (threadIdx.x >> 5) * 2 * a.H;
+    float* sum = reinterpret_cast<float*>(ring);  // [rows of the block][2][H]
+    float* w = sum + rows.place * 2 * a.H;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int col = 8 * (rows.tid + k * rows.threads);
@@ -457,7 +464,7 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512, kWarpRow ? 2 : 1)
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * a.H; i += blockDim.x) {
       float t = sum[i];
-      for (int k = 1; k < kNormRowWarps; ++k) t += sum[k * 2 * a.H + i];
+      for (int k = 1; k < kNormLaneBlock / (kLanes ? kLanes : 32); ++k) t += sum[k * 2 * a.H + i];
       p[i] = t;
     }
   } else {

@@ -121,7 +121,9 @@ class Case:
 
 
 @pytest.mark.parametrize("N,H", [(1, 8), (1, 4096), (2, 248), (3, 264), (7, 1000), (33, 2048),
-                                 (5, 2056), (40, 2880), (17, 8192), (700, 256), (1500, 1024)])
+                                 (5, 2056), (40, 2880), (17, 8192), (700, 256), (1500, 1024),
+                                 (3, 64), (31, 64), (33, 24), (10007, 40), (5, 72), (17, 128),
+                                 (10001, 128), (9, 136), (6001, 512), (3, 520), (2, 4104)])
 def test_sizes(N, H):
     Case(N, H).check()
 
