@@ -50,7 +50,7 @@ enum class CeMode { kFwd, kFwdBwd, kBwd };
 struct CeLayout {
   long long C, Vp, NT, NTh, nchunks;
   int slab_units;
-  size_t off_list, off_share, off_lab, off_kw, off_zlab, off_lse2, off_part, off_zsum, off_h,
+  size_t off_list, off_share, off_lab, off_kw, off_zlab, off_lse2, off_rest, off_part, off_zsum, off_h,
       off_dlog, off_slab, off_dw, total;
 };
 
@@ -102,6 +102,7 @@ CeLayout ce_layout(const fckl_ce_problem* p, bool grads) {
   L.off_kw = take(C * 4);
   L.off_zlab = take(C * 4);
   L.off_lse2 = take(C * 4);
+  L.off_rest = take(C * 4);
   L.off_part = take(C * 2 * L.NT * sizeof(float2));
   L.off_zsum = take(p->label_smoothing > 0.f ? C * 2 * L.NT * 4 : 0);
   L.off_h = take(align_up(C, CM) * p->H * 2);
@@ -196,6 +197,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
   float* kw = static_cast<float*>(at(L.off_kw));
   float* zlab = static_cast<float*>(at(L.off_zlab));
   float* lse2 = static_cast<float*>(at(L.off_lse2));
+  float* rest = static_cast<float*>(at(L.off_rest));
   float2* part = static_cast<float2*>(at(L.off_part));
   float* zsum = static_cast<float*>(at(L.off_zsum));
   __nv_bfloat16* hst = static_cast<__nv_bfloat16*>(at(L.off_h));
@@ -334,11 +336,11 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
           1, std::min<long long>(cdiv(L.Vp, 2048), cdiv(4ll * dev->sms, cap)));
       FCKL_LAUNCH(k_ce_dlogits, dim3(cap, parts), 256, 0, (const float2*)part, zs, NP, rc, V, L.Vp, invT,
                   prob->label_smoothing, prob->z_loss, clist, (const int*)lab, (const float*)zlab,
-                  (const float*)kw, reinterpret_cast<uint4*>(dlog), q.row_loss, q.lse_out,
+                  (const float*)kw, reinterpret_cast<uint4*>(dlog), rest, q.row_loss, q.lse_out,
                   share + row0, (const float*)share, N, ctl, blocks, q.loss);
     } else {
       EpiCeDlogits::Params pb{V, scale2, invT * kLog2e, prob->label_smoothing, 2.f * prob->z_loss, lab, kw, zlab,
-                              lse2, cap};
+                              lse2, rest, cap};
       ProfScope ps(K_CE_DLOGITS, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
       FCKL_CE_GEMM(EpiCeDlogits, mapD_st, pb);
     }
@@ -400,15 +402,17 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     if (q.dH || last) {
       uint4* zdw = last ? static_cast<uint4*>(q.dW) : nullptr;
       const long long vecs = (long long)V * H * (bf16_grads ? 2 : 4) / 16;
-      ProfScope ps(K_DH_OUT, st, 0.0, nr * H * (bf16_grads ? 6.0 : 8.0));
+      ProfScope ps(K_DH_OUT, st, 0.0, nr * H * (bf16_grads ? 8.0 : 10.0));
       if (bf16_grads)
         FCKL_LAUNCH(k_ce_dh_out<__nv_bfloat16>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H, NTh,
                     KBv, dh_pairs, L.slab_units, static_cast<__nv_bfloat16*>(q.dH), zdw, vecs,
-                    (const DeviceCtl*)ctl);
+                    (const DeviceCtl*)ctl, invT, static_cast<const __nv_bfloat16*>(q.W),
+                    (const int*)lab, (const float*)rest);
       else
         FCKL_LAUNCH(k_ce_dh_out<float>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H, NTh, KBv,
                     dh_pairs, L.slab_units, static_cast<float*>(q.dH), zdw, vecs,
-                    (const DeviceCtl*)ctl);
+                    (const DeviceCtl*)ctl, invT, static_cast<const __nv_bfloat16*>(q.W),
+                    (const int*)lab, (const float*)rest);
     }
   }
   if (q.dW && dw_dst != q.dW) {

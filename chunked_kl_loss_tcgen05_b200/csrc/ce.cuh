@@ -459,6 +459,12 @@ __device__ __forceinline__ float ce_label_grad(float k, float q1, float zl, floa
   return fmaf(k, fmaf(q1, 1.f + zl, zl + smooth), -base);
 }
 
+// What bf16 cuts off the label's entry.  That entry carries most of a row's
+// gradient, so k_ce_dh_out adds the rest times the label's row of W in fp32.
+__device__ __forceinline__ float bf16_rest(float g) {
+  return g - __bfloat162float(__float2bfloat16_rn(g));
+}
+
 // Backward without the forward's exponentials (the row-gradient call):
 // recomputed z tile -> G (see the top), rounded once to bf16 and TMA-stored to
 // the chunk's [rows, Vp] block.  Columns in [V, Vp) and the rows behind the last
@@ -477,6 +483,7 @@ struct EpiCeDlogits {
     const float* kw;       // [rows] k_r
     const float* zlab;     // [rows] z at the label
     const float* lse2;     // [rows] log2(e) LSE
+    float* rest;           // [rows] bf16_rest of the label's entry
     int store_rows;        // rows of the store map
   };
   struct State {
@@ -499,6 +506,7 @@ struct EpiCeDlogits {
     if ((unsigned)y < 128u) {
       const float q1 = expm1f(fmaf(p.zlab[row], p.label_scale2, -lse2) * kLn2);  // q_y - 1
       g_y = ce_label_grad(kw, q1, p.zloss2 * lse2 * kLn2, p.smooth, base_mass);
+      p.rest[row] = bf16_rest(g_y);
     }
     const int y0 = w.m0 + quarter * 32;
     const int y_end = min((w.rows + 63) & ~63, p.store_rows);
@@ -789,7 +797,7 @@ __global__ void __launch_bounds__(256)
                  RowCount rc, int V, long long Vp, float invT, float smooth, float zloss,
                  const int32_t* __restrict__ list, const int* __restrict__ lab,
                  const float* __restrict__ zlab, const float* __restrict__ kw,
-                 uint4* __restrict__ dlog, float* __restrict__ row_loss,
+                 uint4* __restrict__ dlog, float* __restrict__ rest, float* __restrict__ row_loss,
                  float* __restrict__ lse_out, float* __restrict__ share,
                  const float* __restrict__ all_shares, long long N, DeviceCtl* ctl,
                  unsigned blocks, float* __restrict__ loss) {
@@ -843,6 +851,7 @@ __global__ void __launch_bounds__(256)
   const float base_mass = k0 * smooth / (float)V;
   const int y = lab[row];
   const float g_y = ce_label_grad(k0, w.q1, zl, smooth, base_mass);
+  if (first && threadIdx.x == 0) rest[row] = bf16_rest(g_y);
   uint4* dr = dlog + (size_t)row * (Vp / 8);
   const long long vecs = Vp / 8, step = 256ll * gridDim.y;
   constexpr int kAhead = 4;  // loads in flight per thread
@@ -886,8 +895,8 @@ __global__ void __launch_bounds__(256)
   if (first) ce_finish_loss(all_shares, N, ctl, blocks, loss);
 }
 
-// dH rows of one chunk: the sum of the row's slabs, in segment order, to the
-// caller's row (zeros for left-out rows), rounded once.  A block takes 512
+// dH rows of one chunk: the sum of the row's slabs, in segment order, and the
+// label's rest, to the caller's row (zeros for left-out rows), rounded once.  A block takes 512
 // columns (blockIdx.y) of a list entry (blockIdx.x).  The number of segments is the one the dH GEMM chose (same inputs).
 // When the whole call kept no row, no dW launch wrote anything: the blocks zero
 // the dw_bytes of dW (dw != nullptr) instead.
@@ -895,7 +904,9 @@ template <class Out>
 __global__ void __launch_bounds__(128)
     k_ce_dh_out(const float* __restrict__ slabs, const int32_t* __restrict__ list, RowCount rc,
                 int H, int NTh, int KB, int slots, int slab_units, Out* __restrict__ dH,
-                uint4* __restrict__ dw, long long dw_vecs, const DeviceCtl* ctl) {
+                uint4* __restrict__ dw, long long dw_vecs, const DeviceCtl* ctl, float invT,
+                const __nv_bfloat16* __restrict__ W, const int* __restrict__ lab,
+                const float* __restrict__ rest) {
   pdl_wait();
   pdl_trigger();
   const int i = blockIdx.x;
@@ -917,11 +928,17 @@ __global__ void __launch_bounds__(128)
   if (j >= H) return;
   const float* src = slabs + (size_t)i * H + j;
   float4 a = *reinterpret_cast<const float4*>(src);
+  const uint2 wy = *reinterpret_cast<const uint2*>(W + (size_t)lab[i] * H + j);
+  const float f = rest[i] * (invT / (float)ctl->n_valid);
 #pragma unroll 4
   for (int s = 1; s < S; ++s) {
     const float4 b = *reinterpret_cast<const float4*>(src + s * pitch);
     a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
   }
+  a.x = fmaf(f, bf16_lo(wy.x), a.x);
+  a.y = fmaf(f, bf16_hi(wy.x), a.y);
+  a.z = fmaf(f, bf16_lo(wy.y), a.z);
+  a.w = fmaf(f, bf16_hi(wy.y), a.w);
   store4(dst + j, a);
 }
 

@@ -11,6 +11,7 @@ from __future__ import annotations
 import dataclasses
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (FcklCeProblem, FcklError, FcklNormProblem, FcklProblem, FCKL_BFLOAT, FCKL_FLOAT,
                FCKL_GRAD_BFLOAT, FCKL_GRAD_FLOAT, FCKL_LABELS_INT, FCKL_LABELS_LONG,
@@ -610,6 +611,7 @@ class FusedCrossEntropy(torch.autograd.Function):
         return value
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         none = (None,) * 6
         if grad_out is None:
@@ -787,6 +789,7 @@ class BlockNorm(torch.autograd.Function):
         return y if block is None else v if y is None else (v, y)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         x, block, post_weight, gate, pre_weight = ctx.saved_tensors
         opts = dict(ctx.opts)
