@@ -339,7 +339,7 @@ def fckl_status_string(status: int) -> str:
 KERNEL_KINDS = ("count_valid", "prep_teacher", "fwd_logits_lse", "merge_loss", "bwd_dlogits",
                 "dH_gemm", "dW_gemm", "finalize", "entropy_gemm", "merge_entropy", "gather_rows",
                 "scatter_rows", "select_rows", "zero_dw", "ce_logits", "ce_dlogits", "dH_rows",
-                "dW_round", "norm_fwd", "norm_bwd", "norm_sum", "ce_scale",
+                "norm_fwd", "norm_bwd", "norm_sum", "ce_scale",
                 "dH_dW_gemm")
 
 

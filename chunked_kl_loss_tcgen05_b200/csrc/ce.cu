@@ -358,7 +358,9 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     SchedArgs sa_w{SCHED_TILES, NTh, 0, 1, MTv, rc, d3d, h3d, 0, narrow_h, 0};
     sa_w.poll_ns = kPollNs;
     const EpiCeDW::Params pw{V, H, invT, ctl};
-    const EpiCeDWSum::Params ps_w{V, H, invT, c > 0 ? 1 : 0, ctl};
+    const EpiCeDWSum::Params ps_w{V, H, invT, c > 0 ? 1 : 0, ctl, (int)(row0 + cap),
+                                  static_cast<const float*>(dw_dst),
+                                  bf16_grads ? static_cast<__nv_bfloat16*>(q.dW) : nullptr};
     const double dh_bytes = 2.0 * nr * V + 2.0 * (double)V * H + 4.0 * nr * H;
     const double dw_bytes = 2.0 * nr * (V + H) + (dw_direct16 ? 2.0 : c > 0 ? 8.0 : 4.0) * V * H;
     const bool two = q.dH && q.dW && L.nchunks == 1 && cap <= kTwoRows;
@@ -398,7 +400,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       }
     }
     // the last chunk's blocks zero dW when no row was kept
-    const bool last = c + 1 == L.nchunks && q.dW && dw_dst == q.dW;
+    const bool last = c + 1 == L.nchunks && q.dW;
     if (q.dH || last) {
       uint4* zdw = last ? static_cast<uint4*>(q.dW) : nullptr;
       const long long vecs = (long long)V * H * (bf16_grads ? 2 : 4) / 16;
@@ -414,12 +416,6 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
                     (const DeviceCtl*)ctl, invT, static_cast<const __nv_bfloat16*>(q.W),
                     (const int*)lab, (const float*)rest);
     }
-  }
-  if (q.dW && dw_dst != q.dW) {
-    const long long n4 = (long long)V * H / 4;
-    ProfScope ps(K_DW_OUT, st, 0.0, n4 * 24.0);
-    FCKL_LAUNCH(k_ce_dw_out, (int)std::min<long long>(cdiv(n4, 256), (long long)dev->sms * 8), 256,
-                0, (const float4*)dw_dst, n4, static_cast<uint2*>(q.dW), (const DeviceCtl*)ctl);
   }
   return cudaGetLastError() == cudaSuccess ? FCKL_OK : FCKL_ERR_CUDA;
 }

@@ -154,14 +154,14 @@ cudaError_t launch(bool pdl, void (*kernel)(KArgs...), dim3 grid, int block, siz
 // ---------------------------------------------------------------- profiling
 enum Kind {
   K_COUNT, K_PREP, K_FWD, K_MERGE, K_BWD, K_DH, K_DW, K_FINAL, K_ENT, K_ENT_MERGE, K_GATHER,
-  K_SCATTER, K_SELECT, K_ZERO_DW, K_CE_FWD, K_CE_DLOGITS, K_DH_OUT, K_DW_OUT,
+  K_SCATTER, K_SELECT, K_ZERO_DW, K_CE_FWD, K_CE_DLOGITS, K_DH_OUT,
   K_NORM_FWD, K_NORM_BWD, K_NORM_SUM, K_CE_SCALE, K_DHW, K_NKINDS
 };
 inline const char* const kKindName[K_NKINDS] = {
     "count_valid", "prep_teacher", "fwd_logits_lse", "merge_loss", "bwd_dlogits",
     "dH_gemm",     "dW_gemm",      "finalize",       "entropy_gemm", "merge_entropy",
     "gather_rows", "scatter_rows", "select_rows", "zero_dw", "ce_logits", "ce_dlogits",
-    "dH_rows", "dW_round", "norm_fwd", "norm_bwd", "norm_sum",
+    "dH_rows", "norm_fwd", "norm_bwd", "norm_sum",
     "ce_scale", "dH_dW_gemm"};
 struct ProfRec {
   int kind;

@@ -458,8 +458,7 @@ const char* fckl_status_string(fckl_status status);
  *        9 merge_entropy, 10 gather_rows, 11 scatter_rows (reserved: gathered
  *        rows write their results in place, no kernel of this kind runs),
  *        12 select_rows, 13 zero_dw, 14 ce_logits, 15 ce_dlogits, 16 dH_rows,
- *        17 dW_round, 18 norm_fwd, 19 norm_bwd, 20 norm_sum,
- *        21 ce_scale, 22 dH_dW_gemm. */
+ *        17 norm_fwd, 18 norm_bwd, 19 norm_sum, 20 ce_scale, 21 dH_dW_gemm. */
 typedef struct {
   char name[32];     /* kernel kind, e.g. "fwd_logits_lse" */
   int64_t launches;  /* launches recorded */
