@@ -9,6 +9,7 @@ upstream gradient in backward.
 from __future__ import annotations
 
 import dataclasses
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -426,38 +427,58 @@ def _placed(index, tensors):
     return index >= 0
 
 
+@functools.lru_cache(maxsize=256)
+def _ce_problem(*fields):
+    """The problem of these sizes and options, and its workspace sizes without and
+    with gradients."""
+    prob = FcklCeProblem(*fields)
+    return prob, fckl_ce_workspace_bytes(prob, False), fckl_ce_workspace_bytes(prob, True)
+
+
+_norm_struct = functools.lru_cache(maxsize=256)(FcklNormProblem)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace_bytes(prob_fields):
+    return fckl_block_norm_workspace_bytes(FcklNormProblem(*prob_fields))
+
+
 def _ce_setup(hidden, W, labels, rows, T, label_smoothing, z_loss, ignore_index, reduction, chunk,
               n_valid_total, grad_dtype, workspace, gradients):
     """Checks, the problem and the workspace of a cross-entropy call.  ``rows``:
     (name, tensor or None) of the per-row float32 inputs."""
-    hidden, W = _bits(hidden), _bits(W)
-    _check_shapes(hidden, W)
+    if hidden.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        hidden, W = _bits(hidden), _bits(W)
+    if hidden.dim() != 2 or W.dim() != 2 or W.shape[1] != hidden.shape[1]:
+        _check_shapes(hidden, W)
     N, H = hidden.shape
+    index = hidden.get_device()
+    placed = _placed(index, (hidden, W, labels))
     if labels.dtype not in _LABEL_TYPES:
         raise TypeError(f"labels must be int32 or int64, got {labels.dtype}")
-    if labels.dim() != 1 or labels.shape[0] != N:
+    if labels.shape != (N,):
         raise ValueError(f"labels must be [N={N}], got {tuple(labels.shape)}")
     for name, t in rows:
-        if t is not None and (t.dtype != torch.float32 or t.shape != (N,)):
-            raise TypeError(f"{name} must be a float32 tensor [N={N}]")
+        if t is not None:
+            if t.dtype != torch.float32 or t.shape != (N,):
+                raise TypeError(f"{name} must be a float32 tensor [N={N}]")
+            placed = placed and t.get_device() == index and t.is_contiguous()
     if reduction not in _REDUCTIONS:
         raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}, got {reduction!r}")
     if grad_dtype not in _GRAD_TYPES:
         raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
-    if not _placed(hidden.get_device(), (hidden, W, labels) + tuple(t for _, t in rows)):
+    if not placed:
         _check_placement(True, [("hidden", hidden), ("W", W), ("labels", labels)] + list(rows))
-    prob = FcklCeProblem(N, H, W.shape[0], T, label_smoothing, z_loss, _REDUCTIONS[reduction],
-                         ignore_index, chunk, n_valid_total, _LABEL_TYPES[labels.dtype],
-                         _GRAD_TYPES[grad_dtype])
-    dev = hidden.device
+    prob, *nbytes = _ce_problem(N, H, W.shape[0], T, label_smoothing, z_loss,
+                                _REDUCTIONS[reduction], ignore_index, chunk, n_valid_total,
+                                _LABEL_TYPES[labels.dtype], _GRAD_TYPES[grad_dtype])
     if workspace is None:
-        nbytes = fckl_ce_workspace_bytes(prob, gradients)
-        if nbytes == 0:
+        if nbytes[gradients] == 0:
             raise FcklError(1, "fckl_ce_workspace_bytes")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(nbytes[gradients], dtype=torch.uint8, device=hidden.device)
     elif (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
-          or workspace.device != dev):
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+          or workspace.device != hidden.device):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {hidden.device}")
     return hidden, W, prob, workspace
 
 
@@ -689,7 +710,7 @@ def _norm_checks(x, block, post_weight, gate, pre_weight, dy=None, dv=None):
 
 def _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps, weight_offset,
                   dy=None, dv=None):
-    """The checked problem of a block_norm call.  One quick pass over the tensors;
+    """The fields of a block_norm call's problem, checked.  One quick pass over the tensors;
     only what it does not accept goes through the checks that name the fault."""
     shape, index, wt, ok = x.shape, x.get_device(), None, x.dim() == 2
     if ok:
@@ -705,10 +726,10 @@ def _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps
               and _placed(index, (x, block, post_weight, gate, pre_weight, dy, dv)))
     if not ok:
         _norm_checks(x, block, post_weight, gate, pre_weight, dy, dv)
-    return FcklNormProblem(shape[0], shape[1], scale, eps, weight_offset,
-                           (FCKL_NORM_POST if post else 0) | (FCKL_NORM_PRE if pre else 0),
-                           _REAL_TYPES[x.dtype], _REAL_TYPES[wt] if wt else FCKL_FLOAT,
-                           FCKL_BFLOAT if dy is None else _REAL_TYPES[dy.dtype])
+    return (shape[0], shape[1], scale, eps, weight_offset,
+            (FCKL_NORM_POST if post else 0) | (FCKL_NORM_PRE if pre else 0),
+            _REAL_TYPES[x.dtype], _REAL_TYPES[wt] if wt else FCKL_FLOAT,
+            FCKL_BFLOAT if dy is None else _REAL_TYPES[dy.dtype])
 
 
 def block_norm_fwd(x, block=None, post_weight=None, gate=None, pre_weight=None, scale=1.0,
@@ -724,12 +745,12 @@ def block_norm_fwd(x, block=None, post_weight=None, gate=None, pre_weight=None, 
     bfloat16); v is x itself without a block and None without ``want_residual``;
     y is None without ``pre``."""
     post = post_weight is not None if post is None else bool(post)
-    prob = _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps,
-                         weight_offset)
+    fields = _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps,
+                           weight_offset)
     dev = x.device
     v = torch.empty_like(x) if block is not None and (want_residual or not pre) else None
     y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if pre else None
-    st = _on_device(dev.index, fckl_block_norm_fwd, prob, x.data_ptr(), _ptr(block),
+    st = _on_device(dev.index, fckl_block_norm_fwd, _norm_struct(*fields), x.data_ptr(), _ptr(block),
                     _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(v), _ptr(y))
     if st != FCKL_OK:
         raise FcklError(st, "fckl_block_norm_fwd")
@@ -748,13 +769,13 @@ def block_norm_bwd(x, block=None, dy=None, dv=None, post_weight=None, gate=None,
         raise ValueError("dy is required with a pre-norm")
     if not pre and (dy is not None or dv is None):
         raise ValueError("without a pre-norm there is dv and no dy")
-    prob = _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps,
-                         weight_offset, dy, dv)
-    dev = x.device
+    fields = _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps,
+                           weight_offset, dy, dv)
+    dev, H = x.device, fields[1]
     if workspace is None:
-        nbytes = fckl_block_norm_workspace_bytes(prob)
+        nbytes = _norm_workspace_bytes(fields)
         if nbytes == 0:
-            raise FcklError(1 if prob.H % 8 == 0 and prob.H <= 8192 else 2,
+            raise FcklError(1 if H % 8 == 0 and H <= 8192 else 2,
                             "fckl_block_norm_workspace_bytes")
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     elif (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
@@ -762,11 +783,15 @@ def block_norm_bwd(x, block=None, dy=None, dv=None, post_weight=None, gate=None,
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     dx = torch.empty_like(x) if want[0] else None
     dblock = torch.empty_like(block) if want[1] and block is not None else None
-    dws = [torch.empty(prob.H, dtype=torch.float32, device=dev) if on and w is not None else None
-           for on, w in zip(want[2:], (post_weight, gate, pre_weight))]
-    if dx is None and dblock is None and not any(d is not None for d in dws):
+    dws = [None, None, None]
+    given = [i for i, w in enumerate((post_weight, gate, pre_weight)) if w is not None and want[2 + i]]
+    if given:
+        for i, row in zip(given, torch.empty(len(given), H, dtype=torch.float32,
+                                             device=dev).unbind()):
+            dws[i] = row
+    elif dx is None and dblock is None:
         return None, None, None, None, None
-    st = _on_device(dev.index, fckl_block_norm_bwd, prob, x.data_ptr(), _ptr(block),
+    st = _on_device(dev.index, fckl_block_norm_bwd, _norm_struct(*fields), x.data_ptr(), _ptr(block),
                     _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(dy), _ptr(dv), _ptr(dx),
                     _ptr(dblock), _ptr(dws[0]), _ptr(dws[1]), _ptr(dws[2]), workspace.data_ptr(),
                     workspace.numel())
