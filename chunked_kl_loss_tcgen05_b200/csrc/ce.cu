@@ -116,6 +116,10 @@ CeLayout ce_layout(const fckl_ce_problem* p, bool grads) {
   return L;
 }
 
+// Chunks of so few rows that a warp a row would leave SMs idle merge them with a
+// block each (one row against 128256 columns: 9.6 us with a warp, 6.5 with a block).
+bool ce_block_rows(long long cap) { return cap <= 148 * kCeWarps; }
+
 struct CeRequest {
   CeMode mode = CeMode::kFwd;
   const fckl_ce_problem* prob = nullptr;
@@ -245,7 +249,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
   unsigned blocks = 0;
   for (long long c = 0; c < L.nchunks; ++c) {
     const long long cap = std::min(L.C, N - c * L.C);
-    blocks += (unsigned)(q.mode == CeMode::kFwd ? cdiv(cap, kCeWarps) : cap);
+    blocks += (unsigned)(q.mode == CeMode::kFwd && !ce_block_rows(cap) ? cdiv(cap, kCeWarps) : cap);
   }
 
   CUtensorMap mapW_k, mapW_mn, mapdW, mapSlab;
@@ -313,10 +317,12 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
         }
       }
       ProfScope ps(K_MERGE, st, 0.0, nr * (NT * 8.0 + 28.0));
-      FCKL_LAUNCH(k_ce_merge, (int)cdiv(cap, kCeWarps), kCeWarps * 32, 0, (const float2*)part, zs,
-                  NP, rc, cap, V, invT, prob->label_smoothing, prob->z_loss, clist,
-                  (const float*)zlab, (const float*)kw, q.row_loss, q.lse_out, share + row0,
-                  (const float*)share, N, ctl, blocks, q.loss);
+      const bool block_row = ce_block_rows(cap);
+      FCKL_LAUNCH(block_row ? k_ce_merge<true> : k_ce_merge<false>,
+                  block_row ? cap : (int)cdiv(cap, kCeWarps), 256, 0, (const float2*)part, zs, NP,
+                  rc, cap, V, invT, prob->label_smoothing, prob->z_loss, clist, (const float*)zlab,
+                  (const float*)kw, q.row_loss, q.lse_out, share + row0, (const float*)share, N, ctl,
+                  blocks, q.loss);
       continue;
     }
     if (q.mode == CeMode::kFwdBwd) {

@@ -793,11 +793,51 @@ struct CeRow {
   }
 };
 
+// Max and sum of a row's partials (and its sum of z), on all threads of the row:
+// a warp, or a block of 256 threads.
+struct CeMerged {
+  float M, S, Z;
+};
+template <bool kBlockRow>
+__device__ __forceinline__ CeMerged ce_merge_row(const float2* __restrict__ pr,
+                                                 const float* __restrict__ zr, int NP) {
+  constexpr int kThreads = kBlockRow ? 256 : 32;
+  const int tid = threadIdx.x % kThreads;
+  float M = -INFINITY, S = 0.f, Z = 0.f;
+#pragma unroll 4
+  for (int t = tid; t < NP; t += kThreads) {
+    const float2 q = pr[t];
+    const float nm = fmaxf(M, q.x);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    S = S * exp2f(M - ref) + q.y * exp2f(q.x - ref);
+    M = nm;
+    if (zr) Z += zr[t];
+  }
+  const float Mw = warp_max(M);
+  S = warp_sum(S * exp2f(M - (Mw == -INFINITY ? 0.f : Mw)));
+  if (zr) Z = warp_sum(Z);
+  if constexpr (!kBlockRow) return CeMerged{Mw, S, Z};
+  __shared__ float red[3][8];
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) { red[0][warp] = Mw; red[1][warp] = S; red[2][warp] = Z; }
+  __syncthreads();
+  CeMerged m{red[0][0], 0.f, 0.f};
+#pragma unroll
+  for (int k = 1; k < 8; ++k) m.M = fmaxf(m.M, red[0][k]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    m.S += red[1][k] * exp2f(red[0][k] - (m.M == -INFINITY ? 0.f : m.M));
+    m.Z += red[2][k];
+  }
+  return m;
+}
+
 // Merges the tile partials of each row into its LSE and row loss.  All rows of
 // the chunk's part of the list write the caller's row loss and LSE (0 for
 // left-out rows) and their share k_r l_r of the loss (list order).  One warp
-// per row.
-__global__ void __launch_bounds__(kCeWarps * 32)
+// per row, or, when the rows are too few to fill the SMs so, one block.
+template <bool kBlockRow>
+__global__ void __launch_bounds__(256)
     k_ce_merge(const float2* __restrict__ partials, const float* __restrict__ zsum, int NP,
                RowCount rc, int cap, int V, float invT, float smooth, float zloss,
                const int32_t* __restrict__ list, const float* __restrict__ zlab,
@@ -807,29 +847,20 @@ __global__ void __launch_bounds__(kCeWarps * 32)
                float* __restrict__ loss) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kCeWarps + (threadIdx.x >> 5);
+  const int row = kBlockRow ? blockIdx.x : blockIdx.x * kCeWarps + (threadIdx.x >> 5);
+  const bool writes = kBlockRow ? threadIdx.x == 0 : (threadIdx.x & 31) == 0;
   if (row < cap) {
     float l = 0.f, lse = 0.f, part = 0.f;
     if (row < rc.get()) {
-      const float2* pr = partials + (size_t)row * NP;
-      float M = -INFINITY;
-      for (int t = lane; t < NP; t += 32) M = fmaxf(M, pr[t].x);
-      M = warp_max(M);
-      float S = 0.f, Z = 0.f;
-      for (int t = lane; t < NP; t += 32) {
-        const float2 q = pr[t];
-        S += q.y * exp2f(q.x - (M == -INFINITY ? 0.f : M));
-        if (zsum) Z += zsum[(size_t)row * NP + t];
-      }
-      S = warp_sum(S);
-      if (zsum) Z = warp_sum(Z);
-      const CeRow w(M, S, zlab[row] * (invT * kLog2e), Z / (float)V * invT, smooth, zloss);
+      const CeMerged m =
+          ce_merge_row<kBlockRow>(partials + (size_t)row * NP,
+                                  zsum ? zsum + (size_t)row * NP : nullptr, NP);
+      const CeRow w(m.M, m.S, zlab[row] * (invT * kLog2e), m.Z / (float)V * invT, smooth, zloss);
       l = w.loss;
       lse = w.lse;
       part = kw[row] * l;
     }
-    if (lane == 0) {
+    if (writes) {
       const int r = list[row];
       if (row_loss) row_loss[r] = l;
       if (lse_out) lse_out[r] = lse;
@@ -854,10 +885,9 @@ __global__ void __launch_bounds__(256, 4)
                  float* __restrict__ lse_out, float* __restrict__ share,
                  const float* __restrict__ all_shares, long long N, DeviceCtl* ctl,
                  unsigned blocks, float* __restrict__ loss) {
-  __shared__ float red[3][8];
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x;
   const bool first = blockIdx.y == 0;  // the row's block that writes its outputs
   const int r = list[row];
   if (row >= rc.get()) {
@@ -870,30 +900,8 @@ __global__ void __launch_bounds__(256, 4)
     return;
   }
   const float2* pr = partials + (size_t)row * NP;
-  float M = -INFINITY, S = 0.f, Z = 0.f;
-  for (int t = threadIdx.x; t < NP; t += 256) {
-    const float2 q = pr[t];
-    const float nm = fmaxf(M, q.x);
-    const float ref = nm == -INFINITY ? 0.f : nm;
-    S = S * exp2f(M - ref) + q.y * exp2f(q.x - ref);
-    M = nm;
-    if (zsum) Z += zsum[(size_t)row * NP + t];
-  }
-  const float Mw = warp_max(M);
-  S = warp_sum(S * exp2f(M - (Mw == -INFINITY ? 0.f : Mw)));
-  if (zsum) Z = warp_sum(Z);
-  if (lane == 0) { red[0][warp] = Mw; red[1][warp] = S; red[2][warp] = Z; }
-  __syncthreads();
-  M = red[0][0];
-#pragma unroll
-  for (int k = 1; k < 8; ++k) M = fmaxf(M, red[0][k]);
-  S = Z = 0.f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    S += red[1][k] * exp2f(red[0][k] - (M == -INFINITY ? 0.f : M));
-    Z += red[2][k];
-  }
-  const CeRow w(M, S, zlab[row] * (invT * kLog2e), Z / (float)V * invT, smooth, zloss);
+  const CeMerged mg = ce_merge_row<true>(pr, zsum ? zsum + (size_t)row * NP : nullptr, NP);
+  const CeRow w(mg.M, mg.S, zlab[row] * (invT * kLog2e), mg.Z / (float)V * invT, smooth, zloss);
   const float L2 = w.L2, k0 = kw[row];
   if (first && threadIdx.x == 0) {
     if (row_loss) row_loss[r] = w.loss;
