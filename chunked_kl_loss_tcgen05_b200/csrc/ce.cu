@@ -412,13 +412,13 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       const long long vecs = (long long)V * H * (bf16_grads ? 2 : 4) / 16;
       ProfScope ps(K_DH_OUT, st, 0.0, nr * H * (bf16_grads ? 8.0 : 10.0));
       if (bf16_grads)
-        FCKL_LAUNCH(k_ce_dh_out<__nv_bfloat16>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H, NTh,
-                    KBv, dh_pairs, L.slab_units, static_cast<__nv_bfloat16*>(q.dH), zdw, vecs,
+        FCKL_LAUNCH(k_ce_dh_out<__nv_bfloat16>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H,
+                    static_cast<__nv_bfloat16*>(q.dH), zdw, vecs,
                     (const DeviceCtl*)ctl, invT, static_cast<const __nv_bfloat16*>(q.W),
                     (const int*)lab, (const float*)rest);
       else
-        FCKL_LAUNCH(k_ce_dh_out<float>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H, NTh, KBv,
-                    dh_pairs, L.slab_units, static_cast<float*>(q.dH), zdw, vecs,
+        FCKL_LAUNCH(k_ce_dh_out<float>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H,
+                    static_cast<float*>(q.dH), zdw, vecs,
                     (const DeviceCtl*)ctl, invT, static_cast<const __nv_bfloat16*>(q.W),
                     (const int*)lab, (const float*)rest);
     }

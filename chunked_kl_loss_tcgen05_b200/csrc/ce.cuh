@@ -956,15 +956,15 @@ __global__ void __launch_bounds__(256, 4)
   if (first) ce_finish_loss(all_shares, N, ctl, blocks, loss);
 }
 
-// dH rows of one chunk: the sum of the row's slabs, in segment order, and the
-// label's rest, to the caller's row (zeros for left-out rows), rounded once.  A block takes 512
-// columns (blockIdx.y) of a list entry (blockIdx.x).  The number of segments is the one the dH GEMM chose (same inputs).
-// When the whole call kept no row, no dW launch wrote anything: the blocks zero
-// the dw_bytes of dW (dw != nullptr) instead.
+// dH rows of one chunk: the sum of the row's slabs, in segment order (the dH GEMM
+// left their number in the control block), and the label's rest, to the caller's
+// row (zeros for left-out rows), rounded once.  A block takes 512 columns
+// (blockIdx.y) of a list entry (blockIdx.x).  When the whole call kept no row, no
+// dW launch wrote anything: the blocks zero dW (dw_vecs vectors at dw, if given).
 template <class Out>
 __global__ void __launch_bounds__(128)
     k_ce_dh_out(const float* __restrict__ slabs, const int32_t* __restrict__ list, RowCount rc,
-                int H, int NTh, int KB, int slots, int slab_units, Out* __restrict__ dH,
+                int H, Out* __restrict__ dH,
                 uint4* __restrict__ dw, long long dw_vecs, const DeviceCtl* ctl, float invT,
                 const __nv_bfloat16* __restrict__ W, const int* __restrict__ lab,
                 const float* __restrict__ rest) {
@@ -983,10 +983,9 @@ __global__ void __launch_bounds__(128)
     if (j < H) store4(dst + j, make_float4(0, 0, 0, 0));
     return;
   }
-  const int MT = (n + PM - 1) / PM;
-  const int S = choose_split_warp(MT * NTh, KB, slots, slab_units);
-  const size_t pitch = (size_t)MT * PM * H;
   if (j >= H) return;
+  const int S = ctl->split;
+  const size_t pitch = (size_t)((n + PM - 1) / PM) * PM * H;
   const float* src = slabs + (size_t)i * H + j;
   float4 a = *reinterpret_cast<const float4*>(src);
   const uint2 wy = *reinterpret_cast<const uint2*>(W + (size_t)lab[i] * H + j);

@@ -318,6 +318,8 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap& tmA, const CUt
   cluster_sync_all();  // barriers of both CTAs initialised before any remote use
   tc_fence_after();
   if (!sa.early) pdl_wait();
+  // for the kernel that sums the slabs
+  if (sa.slab_units > 0 && cluster == 0 && leader && threadIdx.x == 0) ca.ctl->split = *split_slot;
   pdl_trigger();
   const uint32_t tmem_base = *tmem_slot;
   const WaitCtx wc{ca.timeout_ns, ca.ctl, abort_flag};

@@ -24,7 +24,8 @@ struct DeviceCtl {
   int32_t n_rows;     // rows a masked call compacted (its local valid rows)
   int32_t block_count[kCompactBlocks];  // valid rows per compaction block
   uint32_t ticket;    // blocks of the row kernels that have left their loss shares
-  uint32_t pad[59 - kCompactBlocks];
+  int32_t split;      // k segments of the last GEMM that stored them to slabs
+  uint32_t pad[58 - kCompactBlocks];
 };
 static_assert(sizeof(DeviceCtl) == 256, "control block is 256 bytes");
 
