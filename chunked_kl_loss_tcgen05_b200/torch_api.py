@@ -673,6 +673,8 @@ def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_sm
     if norm is not None:
         hidden = norm(hidden)
     opts = dict(T=T, label_smoothing=label_smoothing, z_loss=z_loss, chunk=chunk)
+    if not torch.is_grad_enabled():  # (inside a Function's forward this cannot be told)
+        hidden, W = hidden.detach(), W.detach()
     return FusedCrossEntropy.apply(hidden, W, labels, row_weight, reduction, ignore_index, check,
                                    opts)
 

@@ -22,8 +22,9 @@ import torch
 
 import oracle
 import synth
-from chunked_kl_loss_tcgen05_b200 import (FCKL_ERR_BAD_INDEX, FcklCeProblem, FcklError,
-                                          fckl_ce_workspace_bytes)
+from chunked_kl_loss_tcgen05_b200 import (FCKL_ERR_BAD_INDEX, FCKL_OK, FcklCeProblem, FcklError,
+                                          fckl_ce_workspace_bytes, fckl_profile_begin,
+                                          fckl_profile_end, fckl_scale_gradient)
 from chunked_kl_loss_tcgen05_b200.torch_api import (fused_ce_bwd, fused_ce_fwd, fused_ce_fwd_bwd,
                                                     fused_cross_entropy_loss)
 
@@ -417,3 +418,114 @@ def test_offsets_past_31_bits():
         assert err.item() <= 6e-3, (v0, err.item())
     ref = sum(G[:, i:i + 20000] @ W[i:i + 20000].double() for i in range(0, V, 20000))
     assert ((dH.double() - ref).norm() / ref.norm()).item() <= 6e-3
+
+
+@pytest.mark.parametrize("chunk", [1, 2, 5, 64, 1000])
+def test_chunks_of_any_size(chunk):
+    c = Case(70, 72, 300, ignored=0.3)
+    o, og = c.oracle(), c.oracle(row_grad=c.g)
+    for gd in (torch.float32, torch.bfloat16):
+        loss, rows, dH, dW = fused_ce_fwd_bwd(c.hidden, c.W, c.labels, chunk=chunk, grad_dtype=gd)
+        check_losses(c, o, loss, rows)
+        check_grads(c, o, dH, dW)
+        _, _, lse = fused_ce_fwd(c.hidden, c.W, c.labels, chunk=chunk)
+        check_grads(c, og, *fused_ce_bwd(c.hidden, c.W, c.labels, lse, c.row_grad, chunk=chunk,
+                                         grad_dtype=gd))
+
+
+@pytest.mark.parametrize("V", [1, 2, 7, 9, 64, 127, 128, 129])
+def test_small_vocabularies(V):
+    c = Case(40, 40, V, ignored=0.2)
+    o = c.oracle(label_smoothing=0.3)
+    loss, rows, dH, dW = fused_ce_fwd_bwd(c.hidden, c.W, c.labels, label_smoothing=0.3)
+    check_losses(c, o, loss, rows)
+    check_grads(c, o, dH, dW)
+
+
+def test_very_many_rows():
+    """Rows selected over many blocks, more row tiles than SMs."""
+    c = Case(300_000, 16, 60, ignored=0.5)
+    o = c.oracle(row_weight=c.w, reduction="sum")
+    loss, rows, dH, dW = fused_ce_fwd_bwd(c.hidden, c.W, c.labels, row_weight=c.weight,
+                                          reduction="sum")
+    check_losses(c, o, loss, rows)
+    # 150000 rows add up in dW in fp32: at most 2^-24 of the magnitudes per 16-row step
+    c.dz = lambda T, d=c.dz(1.0): d + 150_000 / 16 * 2.0 ** -24
+    check_grads(c, o, dH, dW)
+
+
+def test_without_gradients_only_the_forward_runs():
+    c = Case(100, 64, 500)
+    h, W = c.hidden.clone().requires_grad_(), c.W.clone().requires_grad_()
+    fckl_profile_begin()
+    with torch.no_grad():
+        loss = fused_cross_entropy_loss(h, W, c.labels)
+    kinds = {k["name"] for k in fckl_profile_end()}
+    assert not loss.requires_grad and "merge_loss" in kinds
+    assert not kinds & {"ce_scale", "dH_gemm", "dW_gemm", "dH_dW_gemm"}
+    check_losses(c, c.oracle(), loss, fused_ce_fwd(c.hidden, c.W, c.labels)[1])
+
+
+def test_negative_and_zero_weights():
+    c = Case(120, 64, 400)
+    c.w[:] = np.random.default_rng(0).standard_normal(120).astype(np.float32)
+    c.w[::5] = 0
+    weight = torch.from_numpy(c.w).cuda()
+    o = c.oracle(row_weight=c.w, reduction="sum", z_loss=1e-2)
+    loss, rows, dH, dW = fused_ce_fwd_bwd(c.hidden, c.W, c.labels, row_weight=weight,
+                                          reduction="sum", z_loss=1e-2)
+    check_grads(c, o, dH, dW)
+    assert abs(loss.item() - o["loss"]) <= 1e-4 * np.abs(c.w * o["row_loss"]).sum()
+
+
+@pytest.mark.parametrize("n", [1, 3, 4, 13, 1027])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("factor", [1.0, 0.3])
+def test_scale_gradient_any_length(n, dtype, factor):
+    t = torch.randn(n + 8, device="cuda").to(dtype)
+    before, f = t.clone(), torch.tensor([factor], device="cuda")
+    st = fckl_scale_gradient(t.data_ptr(), n, int(dtype == torch.bfloat16), f.data_ptr(),
+                             torch.cuda.current_stream().cuda_stream)
+    assert st == FCKL_OK
+    assert torch.equal(t[:n], (before[:n].float() * f).to(dtype))
+    assert torch.equal(t[n:], before[n:])
+
+
+def test_labels_decide_over_infinities():
+    """An overflowed logit of a kept row shows in that row's loss, not elsewhere."""
+    c = Case(50, 64, 300, ignored=0.0)
+    hidden = c.hidden.clone()
+    hidden[7, 3] = float("inf")
+    loss, rows, lse = fused_ce_fwd(hidden, c.W, c.labels)
+    o = c.oracle()
+    keep = np.arange(50) != 7
+    tol = 2 * c.dz(1.0) + 8 * 2.0 ** -22 * (1 + np.abs(o["lse"]).max())
+    assert np.abs(rows.cpu().numpy() - o["row_loss"])[keep].max() <= tol
+    assert not torch.isfinite(rows[7]) and not torch.isfinite(loss).any()
+
+
+def test_host_threads_on_their_own_streams():
+    import threading
+    cases = [Case(256 + 10 * i, 128, 900, seed=i) for i in range(4)]
+    solo = [fused_ce_fwd_bwd(c.hidden, c.W, c.labels) for c in cases]
+    got, torch_err = [None] * 4, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    r = fused_ce_fwd_bwd(cases[i].hidden, cases[i].W, cases[i].labels)
+                torch.cuda.current_stream().synchronize()
+                got[i] = r
+        except Exception as e:  # noqa: BLE001
+            torch_err.append(e)
+
+    torch.cuda.synchronize()
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not torch_err
+    for g, ref in zip(got, solo):
+        assert all(torch.equal(a, b) for a, b in zip(g, ref))
