@@ -534,8 +534,8 @@ def _fused_ce_fwd_bwd(hidden, W, labels, row_weight, T, label_smoothing, z_loss,
         _check_grad_out("dW", dW, (prob.V, prob.H), grad_dtype, dev)
     else:
         loss = torch.empty(1, dtype=torch.float32, device=dev)
-        dH = torch.empty(prob.N, prob.H, dtype=grad_dtype, device=dev) if want[0] else None
-        dW = torch.empty(prob.V, prob.H, dtype=grad_dtype, device=dev) if want[1] else None
+        dH = torch.empty_like(hidden, dtype=grad_dtype) if want[0] else None
+        dW = torch.empty_like(W, dtype=grad_dtype) if want[1] else None
     row_loss = torch.empty(prob.N, dtype=torch.float32, device=dev)
     lse = torch.empty(prob.N, dtype=torch.float32, device=dev) if want_lse else None
     st = _on_device(dev.index, fckl_ce_fwd_bwd, prob, hidden.data_ptr(), W.data_ptr(),
@@ -579,8 +579,8 @@ def fused_ce_bwd(hidden, W, labels, lse, row_grad, T=1.0, label_smoothing=0.0, z
         _check_grad_out("dH", dH, (prob.N, prob.H), grad_dtype, dev)
         _check_grad_out("dW", dW, (prob.V, prob.H), grad_dtype, dev)
     else:
-        dH = torch.empty(prob.N, prob.H, dtype=grad_dtype, device=dev) if want[0] else None
-        dW = torch.empty(prob.V, prob.H, dtype=grad_dtype, device=dev) if want[1] else None
+        dH = torch.empty_like(hidden, dtype=grad_dtype) if want[0] else None
+        dW = torch.empty_like(W, dtype=grad_dtype) if want[1] else None
     st = _on_device(dev.index, fckl_ce_bwd, prob, hidden.data_ptr(), W.data_ptr(),
                     labels.data_ptr(), lse.data_ptr(), row_grad.data_ptr(), _ptr(dH), _ptr(dW),
                     workspace.data_ptr(), workspace.numel())
@@ -751,7 +751,7 @@ def block_norm_fwd(x, block=None, post_weight=None, gate=None, pre_weight=None, 
                            weight_offset)
     dev = x.device
     v = torch.empty_like(x) if block is not None and (want_residual or not pre) else None
-    y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if pre else None
+    y = torch.empty_like(x, dtype=torch.bfloat16) if pre else None
     st = _on_device(dev.index, fckl_block_norm_fwd, _norm_struct(*fields), x.data_ptr(), _ptr(block),
                     _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(v), _ptr(y))
     if st != FCKL_OK:
@@ -785,21 +785,29 @@ def block_norm_bwd(x, block=None, dy=None, dv=None, post_weight=None, gate=None,
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     dx = torch.empty_like(x) if want[0] else None
     dblock = torch.empty_like(block) if want[1] and block is not None else None
-    dws = [None, None, None]
-    given = [i for i, w in enumerate((post_weight, gate, pre_weight)) if w is not None and want[2 + i]]
-    if given:
-        for i, row in zip(given, torch.empty(len(given), H, dtype=torch.float32,
-                                             device=dev).unbind()):
-            dws[i] = row
+    # one allocation for the weights' gradients
+    want1 = want[2] and post_weight is not None
+    wantg = want[3] and gate is not None
+    want2 = want[4] and pre_weight is not None
+    d1 = dg = d2 = None
+    n = want1 + wantg + want2
+    if n:
+        sums = torch.empty(n, H, dtype=torch.float32, device=dev).unbind()
+        if want1:
+            d1 = sums[0]
+        if wantg:
+            dg = sums[1 if want1 else 0]
+        if want2:
+            d2 = sums[-1]
     elif dx is None and dblock is None:
         return None, None, None, None, None
     st = _on_device(dev.index, fckl_block_norm_bwd, _norm_struct(*fields), x.data_ptr(), _ptr(block),
                     _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(dy), _ptr(dv), _ptr(dx),
-                    _ptr(dblock), _ptr(dws[0]), _ptr(dws[1]), _ptr(dws[2]), workspace.data_ptr(),
+                    _ptr(dblock), _ptr(d1), _ptr(dg), _ptr(d2), workspace.data_ptr(),
                     workspace.numel())
     if st != FCKL_OK:
         raise FcklError(st, "fckl_block_norm_bwd")
-    return dx, dblock, dws[0], dws[1], dws[2]
+    return dx, dblock, d1, dg, d2
 
 
 class BlockNorm(torch.autograd.Function):
