@@ -5,7 +5,8 @@
 // with gradients
 //   gather rows -> logits GEMM (and its exponentials) -> merge and dlogits, or,
 //   for given log-sum-exps, gather rows -> logits GEMM (dlogits epilogue),
-//   -> dH GEMM -> dW GEMM -> dH rows.
+//   -> dH GEMM -> dW GEMM -> dH rows.  (Short hidden rows take the forward's steps
+//   and then those of given log-sum-exps.)
 #include <algorithm>
 #include <cmath>
 
@@ -138,6 +139,19 @@ struct CeRequest {
   void* stream = nullptr;
 };
 
+// The dlogits kernel gives a row to a warp instead of blocks where the vocabulary
+// is too small to keep 256 threads busy and the rows fill the SMs.
+bool ce_warp_dlogits(long long V, long long cap) { return V <= 8192 && !ce_block_rows(cap); }
+
+// Whether a training call computes the logits twice after all: with short hidden
+// rows the second product costs less than keeping the exponentials (written,
+// read, written as dlogits), as long as those do not stay in L2.  Graph-timed
+// steps, us, kept and recomputed: 1531 x 384 x 50257 258 and 245, 4096 x 256 x 128256
+// 1260 and 1150, 4096 x 512 x 50257 694 and 693, 1024 x 256 x 32000 102 and 108.
+bool ce_recompute(CeMode mode, const fckl_ce_problem* p, const CeLayout& L) {
+  return mode == CeMode::kFwdBwd && p->H <= 384 && L.C * L.Vp >= (1ll << 26);
+}
+
 template <class E2>
 bool allow_smem_two() {
   return cudaFuncSetAttribute(gemm_two_kernel<EpiCeDH, false, true, E2, true, true>,
@@ -245,11 +259,14 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
                   denom, list, ctl);
     }
   }
+  const bool recompute = ce_recompute(q.mode, prob, L);
   // Blocks of the row kernels that leave loss shares, over all chunks.
   unsigned blocks = 0;
   for (long long c = 0; c < L.nchunks; ++c) {
     const long long cap = std::min(L.C, N - c * L.C);
-    blocks += (unsigned)(q.mode == CeMode::kFwd && !ce_block_rows(cap) ? cdiv(cap, kCeWarps) : cap);
+    const bool warps = q.mode == CeMode::kFwd || recompute ? !ce_block_rows(cap)
+                                                           : ce_warp_dlogits(prob->V, cap);
+    blocks += (unsigned)(warps ? cdiv(cap, kCeWarps) : cap);
   }
 
   CUtensorMap mapW_k, mapW_mn, mapdW, mapSlab;
@@ -305,7 +322,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
 #define FCKL_CE_GEMM(Epi, map, params)                                                       \
   FCKL_LAUNCH((gemm_pair_kernel<Epi, false, false>), Gv, gemm_threads<Epi>(), pair_smem_bytes<Epi>(), \
               mapH_k, mapW_k, map, params, sa_v, ca)
-    if (q.mode == CeMode::kFwd) {
+    if (q.mode == CeMode::kFwd || recompute) {
       {
         ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + nr * NT * 8.0);
         if (smooth) {
@@ -321,11 +338,11 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       FCKL_LAUNCH(block_row ? k_ce_merge<true> : k_ce_merge<false>,
                   block_row ? cap : (int)cdiv(cap, kCeWarps), 256, 0, (const float2*)part, zs, NP,
                   rc, cap, V, invT, prob->label_smoothing, prob->z_loss, clist, (const float*)zlab,
-                  (const float*)kw, q.row_loss, q.lse_out, share + row0, (const float*)share, N, ctl,
-                  blocks, q.loss);
-      continue;
+                  (const float*)kw, recompute ? lse2 : nullptr, q.row_loss, q.lse_out, share + row0,
+                  (const float*)share, N, ctl, blocks, q.loss);
     }
-    if (q.mode == CeMode::kFwdBwd) {
+    if (q.mode == CeMode::kFwd) continue;
+    if (q.mode == CeMode::kFwdBwd && !recompute) {
       {
         ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
         if (smooth) {
@@ -337,17 +354,21 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
         }
       }
       ProfScope ps(K_CE_SCALE, st, 0.0, nr * (V * 4.0 + NT * 16.0));
+      const bool warp_row = ce_warp_dlogits(prob->V, cap);
       // blocks that share a row, so that few rows still fill the SMs
       const unsigned parts = (unsigned)std::max<long long>(
           1, std::min<long long>(cdiv(L.Vp, 2048), cdiv(4ll * dev->sms, cap)));
-      FCKL_LAUNCH(k_ce_dlogits, dim3(cap, parts), 256, 0, (const float2*)part, zs, NP, rc, V, L.Vp, invT,
-                  prob->label_smoothing, prob->z_loss, clist, (const int*)lab, (const float*)zlab,
-                  (const float*)kw, reinterpret_cast<uint4*>(dlog), rest, q.row_loss, q.lse_out,
-                  share + row0, (const float*)share, N, ctl, blocks, q.loss);
+      FCKL_LAUNCH(warp_row ? k_ce_dlogits<false> : k_ce_dlogits<true>,
+                  warp_row ? dim3((unsigned)cdiv(cap, kCeWarps)) : dim3(cap, parts), 256, 0,
+                  (const float2*)part, zs, NP, rc, cap, V, L.Vp, invT, prob->label_smoothing,
+                  prob->z_loss, clist, (const int*)lab, (const float*)zlab, (const float*)kw,
+                  reinterpret_cast<uint4*>(dlog), rest, q.row_loss, q.lse_out, share + row0,
+                  (const float*)share, N, ctl, blocks, q.loss);
     } else {
-      EpiCeDlogits::Params pb{V, scale2, invT * kLog2e, prob->label_smoothing, 2.f * prob->z_loss, lab, kw, zlab,
-                              lse2, rest, cap};
+      EpiCeDlogits::Params pb{V, scale2, invT * kLog2e, prob->label_smoothing,
+                              2.f * prob->z_loss, lab, kw, zlab, lse2, rest, cap};
       ProfScope ps(K_CE_DLOGITS, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
+      sa_v.early = recompute ? 1 : 0;  // its operands were complete before the merge launched
       FCKL_CE_GEMM(EpiCeDlogits, mapD_st, pb);
     }
 #undef FCKL_CE_GEMM

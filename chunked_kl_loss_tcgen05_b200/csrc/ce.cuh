@@ -834,16 +834,16 @@ __device__ __forceinline__ CeMerged ce_merge_row(const float2* __restrict__ pr,
 
 // Merges the tile partials of each row into its LSE and row loss.  All rows of
 // the chunk's part of the list write the caller's row loss and LSE (0 for
-// left-out rows) and their share k_r l_r of the loss (list order).  One warp
-// per row, or, when the rows are too few to fill the SMs so, one block.
+// left-out rows) and their share k_r l_r of the loss (list order); lse2 (if
+// given) is for the recompute GEMM.  One warp per row, or, when the rows are too few to fill the SMs so, one block.
 template <bool kBlockRow>
 __global__ void __launch_bounds__(256)
     k_ce_merge(const float2* __restrict__ partials, const float* __restrict__ zsum, int NP,
                RowCount rc, int cap, int V, float invT, float smooth, float zloss,
                const int32_t* __restrict__ list, const float* __restrict__ zlab,
-               const float* __restrict__ kw, float* __restrict__ row_loss,
-               float* __restrict__ lse_out, float* __restrict__ share,
-               const float* __restrict__ all_shares, long long N, DeviceCtl* ctl, unsigned blocks,
+               const float* __restrict__ kw, float* __restrict__ lse2,
+               float* __restrict__ row_loss, float* __restrict__ lse_out,
+               float* __restrict__ share, const float* __restrict__ all_shares, long long N, DeviceCtl* ctl, unsigned blocks,
                float* __restrict__ loss) {
   pdl_wait();
   pdl_trigger();
@@ -859,6 +859,7 @@ __global__ void __launch_bounds__(256)
       l = w.loss;
       lse = w.lse;
       part = kw[row] * l;
+      if (lse2 && writes) lse2[row] = w.L2;
     }
     if (writes) {
       const int r = list[row];
@@ -872,13 +873,14 @@ __global__ void __launch_bounds__(256)
 
 // Merge of EpiCeStore's partials, as k_ce_merge, and the row's dlogits from the
 // stored exponentials, in place: fp16 E -> bf16 G = kap E 2^(m_t - L2) - targets,
-// rounded once; the label's entry, which E leaves out, from q_y - 1.  gridDim.y blocks
-// share a row (each merges its partials for itself), 16 bytes a thread at a
-// time, four loads ahead.  Bound by HBM: 4 bytes per entry; 4096 x 128256 in 362
+// rounded once; the label's entry, which E leaves out, from q_y - 1.  A row takes a
+// warp (small vocabularies) or gridDim.y blocks (each merges the partials for
+// itself), 16 bytes a thread at a time, four loads ahead.  Bound by HBM: 4 bytes per entry; 4096 x 128256 in 362
 // us, 5.8 TB/s (384 with the registers of 3 blocks an SM instead of 4).
+template <bool kBlockRow>
 __global__ void __launch_bounds__(256, 4)
     k_ce_dlogits(const float2* __restrict__ partials, const float* __restrict__ zsum, int NP,
-                 RowCount rc, int V, long long Vp, float invT, float smooth, float zloss,
+                 RowCount rc, int cap, int V, long long Vp, float invT, float smooth, float zloss,
                  const int32_t* __restrict__ list, const int* __restrict__ lab,
                  const float* __restrict__ zlab, const float* __restrict__ kw,
                  uint4* __restrict__ dlog, float* __restrict__ rest, float* __restrict__ row_loss,
@@ -887,71 +889,71 @@ __global__ void __launch_bounds__(256, 4)
                  unsigned blocks, float* __restrict__ loss) {
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x;
-  const bool first = blockIdx.y == 0;  // the row's block that writes its outputs
-  const int r = list[row];
-  if (row >= rc.get()) {
-    if (first && threadIdx.x == 0) {
-      if (row_loss) row_loss[r] = 0.f;
-      if (lse_out) lse_out[r] = 0.f;
-      share[row] = 0.f;
+  constexpr int kThreads = kBlockRow ? 256 : 32;
+  const int row = kBlockRow ? blockIdx.x : blockIdx.x * kCeWarps + (threadIdx.x >> 5);
+  const int tid = threadIdx.x % kThreads;
+  const bool first = blockIdx.y == 0;  // of the row's blocks: writes the row's outputs
+  if (row < rc.get()) {
+    const float2* pr = partials + (size_t)row * NP;
+    const CeMerged mg = ce_merge_row<kBlockRow>(pr, zsum ? zsum + (size_t)row * NP : nullptr, NP);
+    const CeRow w(mg.M, mg.S, zlab[row] * (invT * kLog2e), mg.Z / (float)V * invT, smooth, zloss);
+    const float L2 = w.L2, k0 = kw[row];
+    if (first && tid == 0) {
+      const int r = list[row];
+      if (row_loss) row_loss[r] = w.loss;
+      if (lse_out) lse_out[r] = w.lse;
+      share[row] = k0 * w.loss;
     }
-    if (first) ce_finish_loss(all_shares, N, ctl, blocks, loss);
-    return;
-  }
-  const float2* pr = partials + (size_t)row * NP;
-  const CeMerged mg = ce_merge_row<true>(pr, zsum ? zsum + (size_t)row * NP : nullptr, NP);
-  const CeRow w(mg.M, mg.S, zlab[row] * (invT * kLog2e), mg.Z / (float)V * invT, smooth, zloss);
-  const float L2 = w.L2, k0 = kw[row];
-  if (first && threadIdx.x == 0) {
-    if (row_loss) row_loss[r] = w.loss;
-    if (lse_out) lse_out[r] = w.lse;
-    share[row] = k0 * w.loss;
-  }
-  const float zl = 2.f * zloss * w.lse, kap = fmaf(k0, zl, k0);
-  const float base_mass = k0 * smooth / (float)V;
-  const int y = lab[row];
-  const float g_y = ce_label_grad(k0, w.q1, zl, smooth, base_mass);
-  if (first && threadIdx.x == 0) rest[row] = bf16_rest(g_y);
-  uint4* dr = dlog + (size_t)row * (Vp / 8);
-  const long long vecs = Vp / 8, step = 256ll * gridDim.y;
-  constexpr int kAhead = 4;  // loads in flight per thread
-  for (long long i0 = 256ll * blockIdx.y + threadIdx.x; i0 < vecs; i0 += kAhead * step) {
-    uint4 q[kAhead];
-    float m[kAhead];
+    const float zl = 2.f * zloss * w.lse, kap = fmaf(k0, zl, k0);
+    const float base_mass = k0 * smooth / (float)V;
+    const int y = lab[row];
+    const float g_y = ce_label_grad(k0, w.q1, zl, smooth, base_mass);
+    if (first && tid == 0) rest[row] = bf16_rest(g_y);
+    uint4* dr = dlog + (size_t)row * (Vp / 8);
+    const long long vecs = Vp / 8, step = (long long)kThreads * gridDim.y;
+    constexpr int kAhead = 4;  // loads in flight per thread
+    for (long long i0 = (long long)kThreads * blockIdx.y + tid; i0 < vecs; i0 += kAhead * step) {
+      uint4 q[kAhead];
+      float m[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const long long i = i0 + u * step;
-      if (i < vecs) {
-        q[u] = dr[i];
-        m[u] = pr[i >> 4].x;  // 16 vectors to a half tile
+      for (int u = 0; u < kAhead; ++u) {
+        const long long i = i0 + u * step;
+        if (i < vecs) {
+          q[u] = dr[i];
+          m[u] = pr[i >> 4].x;  // 16 vectors to a half tile
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const long long i = i0 + u * step;
+        if (i >= vecs) break;
+        const float f = kap * ex2_approx(m[u] - L2);
+        const uint32_t bits[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&bits[j]));
+          v[2 * j] = fmaf(f, e.x, -base_mass);
+          v[2 * j + 1] = fmaf(f, e.y, -base_mass);
+        }
+        const int at = y - 8 * (int)i;
+        if ((unsigned)at < 8u) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = j == at ? g_y : v[j];
+        }
+        if (8 * i + 8 > V) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = 8 * i + j < V ? v[j] : 0.f;
+        }
+        dr[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
       }
     }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const long long i = i0 + u * step;
-      if (i >= vecs) break;
-      const float f = kap * ex2_approx(m[u] - L2);
-      const uint32_t bits[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&bits[j]));
-        v[2 * j] = fmaf(f, e.x, -base_mass);
-        v[2 * j + 1] = fmaf(f, e.y, -base_mass);
-      }
-      const int at = y - 8 * (int)i;
-      if ((unsigned)at < 8u) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j == at ? g_y : v[j];
-      }
-      if (8 * i + 8 > V) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 8 * i + j < V ? v[j] : 0.f;
-      }
-      dr[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                         pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    }
+  } else if (first && tid == 0 && row < cap) {
+    const int r = list[row];
+    if (row_loss) row_loss[r] = 0.f;
+    if (lse_out) lse_out[r] = 0.f;
+    share[row] = 0.f;
   }
   if (first) ce_finish_loss(all_shares, N, ctl, blocks, loss);
 }

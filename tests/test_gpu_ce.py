@@ -529,3 +529,20 @@ def test_host_threads_on_their_own_streams():
     assert not torch_err
     for g, ref in zip(got, solo):
         assert all(torch.equal(a, b) for a, b in zip(g, ref))
+
+
+@pytest.mark.parametrize("N,H,V,kw", [
+    (1400, 64, 48000, {}),                                  # logits computed twice
+    (1400, 64, 48000, dict(label_smoothing=0.1, z_loss=1e-3)),
+    (2900, 40, 48001, dict(chunk=1450)),                    # the same in chunks
+    (1300, 72, 700, {}), (1300, 72, 8192, {}),              # a warp a row of dlogits
+    (1184, 72, 700, {}), (1300, 72, 8200, {})])             # just past those
+def test_both_sides_of_every_rule(N, H, V, kw):
+    c = Case(N, H, V, ignored=0.2, std=0.2)
+    w = {k: v for k, v in kw.items() if k != "chunk"}
+    o = c.oracle(row_weight=c.w, **w)
+    loss, rows, dH, dW = fused_ce_fwd_bwd(c.hidden, c.W, c.labels, row_weight=c.weight, **kw)
+    check_losses(c, o, loss, rows, z_loss=w.get("z_loss", 0.0))
+    check_grads(c, o, dH, dW)
+    again = fused_ce_fwd_bwd(c.hidden, c.W, c.labels, row_weight=c.weight, **kw)
+    assert torch.equal(dH, again[2]) and torch.equal(dW, again[3])
