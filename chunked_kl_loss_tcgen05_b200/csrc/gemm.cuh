@@ -146,9 +146,10 @@ struct SchedArgs {
   // barrier: 0 = 2 us (main loops of tens of microseconds), > 0 = this many ns
   // per k-block of the unit, at most 2 us.
   int poll_ns;
-  // 1: the kernel just ahead writes the row count itself, so every thread waits
-  // for it before the count is first read (needs early = 0).  Otherwise the
-  // count is older: complete when the kernel ahead let this one launch.
+  // 1: the kernel just ahead writes the row count itself, so the count is not
+  // read before the wait for that kernel (needs early = 0 and a split factor that
+  // does not depend on the rows).  Otherwise the count is older: complete when the
+  // kernel ahead let this one launch.
   int fresh_rows;
 };
 
@@ -269,12 +270,12 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap& tmA, const CUt
   uint32_t* abort_flag = tmem_slot + 1;
   int* split_slot = reinterpret_cast<int*>(abort_flag + 1);
 
-  if (sa.fresh_rows) pdl_wait();
   // A launch over no rows (a chunk past the last compacted row) has no work:
   // both CTAs of every pair see the same count and leave before setting up
   // barriers or TMEM (still waiting for the kernel ahead, so that completion
-  // keeps implying the completion of everything before).
-  if (sa.rc.get() <= 0) {
+  // keeps implying the completion of everything before).  Where the count is not
+  // there yet, the roles find no unit instead.
+  if (!sa.fresh_rows && sa.rc.get() <= 0) {
     pdl_wait();
     pdl_trigger();
     return;
