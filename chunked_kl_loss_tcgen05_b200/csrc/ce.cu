@@ -19,9 +19,9 @@ using namespace fckl;
 namespace {
 
 // Sleep of an epilogue between polls, per k-block of its unit.  A k-block takes
-// a pair about 280 ns, so this is a tenth of the main loop: 2 us regardless of
-// it, as long loops can afford, cost
-// 1531 x 1024 x 50257 (a step) 476 us against 417.
+// a pair about 280 ns, so this is a tenth of the main loop; 2 us regardless of
+// it, as long loops can afford, cost 476 us against 417 in a step of
+// 1531 x 1024 x 50257.
 constexpr int kPollNs = 30;
 
 // The tensor cores add 16 products at a time to an fp32 accumulator and cut the
@@ -51,8 +51,8 @@ enum class CeMode { kFwd, kFwdBwd, kBwd };
 struct CeLayout {
   long long C, Vp, NT, NTh, nchunks;
   int slab_units;
-  size_t off_list, off_share, off_lab, off_kw, off_zlab, off_lse2, off_rest, off_part, off_zsum, off_h,
-      off_dlog, off_slab, off_dw, total;
+  size_t off_list, off_share, off_lab, off_kw, off_zlab, off_lse2, off_rest, off_part, off_zsum,
+      off_h, off_dlog, off_slab, off_dw, total;
 };
 
 bool valid_ce(const fckl_ce_problem* p) {
@@ -188,7 +188,8 @@ const CeDevice* ce_device() {
     d.ok = major == 10 && minor == 0 && d.sms > 1 && allow_smem<EpiCe<false>, false, false>() &&
            allow_smem<EpiCe<true>, false, false>() &&
            allow_smem<EpiCeStore<false>, false, false>() &&
-           allow_smem<EpiCeStore<true>, false, false>() && allow_smem<EpiCeDlogits, false, false>() &&
+           allow_smem<EpiCeStore<true>, false, false>() &&
+           allow_smem<EpiCeDlogits, false, false>() &&
            allow_smem<EpiCeDH, false, true>() && allow_smem<EpiCeDW, true, true>() &&
            allow_smem<EpiCeDWSum, true, true>() && allow_smem_two<EpiCeDW>() &&
            allow_smem_two<EpiCeDWSum>();
@@ -319,9 +320,9 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     if (grads && !make_map(&mapD_st, dlog, L.Vp, cap, L.Vp * 2, 64, 32)) return FCKL_ERR_CUDA;
     const float* zs = smooth ? zsum : nullptr;
     // The GEMM over h W^T: its row count, hence its work, is read on the device.
-#define FCKL_CE_GEMM(Epi, map, params)                                                       \
-  FCKL_LAUNCH((gemm_pair_kernel<Epi, false, false>), Gv, gemm_threads<Epi>(), pair_smem_bytes<Epi>(), \
-              mapH_k, mapW_k, map, params, sa_v, ca)
+#define FCKL_CE_GEMM(Epi, map, params)                                        \
+  FCKL_LAUNCH((gemm_pair_kernel<Epi, false, false>), Gv, gemm_threads<Epi>(), \
+              pair_smem_bytes<Epi>(), mapH_k, mapW_k, map, params, sa_v, ca)
     if (q.mode == CeMode::kFwd || recompute) {
       {
         ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + nr * NT * 8.0);
@@ -368,7 +369,10 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       EpiCeDlogits::Params pb{V, scale2, invT * kLog2e, prob->label_smoothing,
                               2.f * prob->z_loss, lab, kw, zlab, lse2, rest, cap};
       ProfScope ps(K_CE_DLOGITS, st, flops, 2.0 * (nr + V) * H + 2.0 * nr * V);
-      sa_v.early = recompute ? 1 : 0;  // its operands were complete before the merge launched
+      if (recompute) {  // the operands and the count were complete before the merge launched
+        sa_v.early = 1;
+        sa_v.fresh_rows = 0;
+      }
       FCKL_CE_GEMM(EpiCeDlogits, mapD_st, pb);
     }
 #undef FCKL_CE_GEMM
@@ -394,8 +398,8 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
     const int dh_pairs = two ? std::max(1, pairs * 3 / 8) : pairs;
     if (two) {
       ProfScope ps(K_DHW, st, 2.0 * flops, dh_bytes + dw_bytes);
-      constexpr size_t smem =
-          std::max({pair_smem_bytes<EpiCeDH>(), pair_smem_bytes<EpiCeDW>(), pair_smem_bytes<EpiCeDWSum>()});
+      constexpr size_t smem = std::max({pair_smem_bytes<EpiCeDH>(), pair_smem_bytes<EpiCeDW>(),
+                                        pair_smem_bytes<EpiCeDWSum>()});
       if (dw_direct16)
         FCKL_LAUNCH((gemm_two_kernel<EpiCeDH, false, true, EpiCeDW, true, true>), 2 * pairs,
                     gemm_threads<EpiCeDH>(), smem, mapD_k, mapW_mn, mapSlab, mapD_mn, mapH_mn,
@@ -433,13 +437,13 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       const long long vecs = (long long)V * H * (bf16_grads ? 2 : 4) / 16;
       ProfScope ps(K_DH_OUT, st, 0.0, nr * H * (bf16_grads ? 8.0 : 10.0));
       if (bf16_grads)
-        FCKL_LAUNCH(k_ce_dh_out<__nv_bfloat16>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H,
-                    static_cast<__nv_bfloat16*>(q.dH), zdw, vecs,
+        FCKL_LAUNCH(k_ce_dh_out<__nv_bfloat16>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0,
+                    (const float*)slab, clist, rc, H, static_cast<__nv_bfloat16*>(q.dH), zdw, vecs,
                     (const DeviceCtl*)ctl, invT, static_cast<const __nv_bfloat16*>(q.W),
                     (const int*)lab, (const float*)rest);
       else
-        FCKL_LAUNCH(k_ce_dh_out<float>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0, (const float*)slab, clist, rc, H,
-                    static_cast<float*>(q.dH), zdw, vecs,
+        FCKL_LAUNCH(k_ce_dh_out<float>, dim3(cap, (unsigned)cdiv(H, 512)), 128, 0,
+                    (const float*)slab, clist, rc, H, static_cast<float*>(q.dH), zdw, vecs,
                     (const DeviceCtl*)ctl, invT, static_cast<const __nv_bfloat16*>(q.W),
                     (const int*)lab, (const float*)rest);
     }

@@ -151,12 +151,11 @@ __device__ __forceinline__ float copy_and_dot(const __nv_bfloat16* __restrict__ 
 }
 
 // One chunk's kept rows, gathered: hidden row -> hst[i], label -> lab[i], the
-// label's logit -> zlab[i], the
-// row's factor (weight, upstream gradient, or 1) -> kw[i], and, when the
-// caller gives the log-sum-exps, log2(e) times them -> lse2[i].  The 64 rows
-// behind the last one get zero hidden rows: the dW GEMM reads whole blocks of
-// 64 rows.  (Gathering, instead of masking in place, keeps what a left-out row
-// holds -- NaN, say -- away from the products.)
+// label's logit -> zlab[i], the row's factor (weight, upstream gradient, or 1) ->
+// kw[i], and, when the caller gives the log-sum-exps, log2(e) times them ->
+// lse2[i].  The 64 rows behind the last one get zero hidden rows: the dW GEMM
+// reads whole blocks of 64 rows.  (Gathering, instead of masking in place, keeps
+// what a left-out row holds -- NaN, say -- away from the products.)
 template <class Label>
 __global__ void __launch_bounds__(128)
     k_ce_gather(const int32_t* __restrict__ list, RowCount rc, int H,
@@ -249,12 +248,14 @@ __global__ void __launch_bounds__(128)
 
 // ---------------------------------------------------------------- epilogues
 // All with eight warps: a thread owns one accumulator row and one half (128
-// columns) of the tile.  At H = 1024 a tile's main loop takes about 8000 cycles,
-// and four warps took longer than that over its exponentials, which come one a
-// cycle from each SM quarter's special-function unit only if two warps take
-// turns.  The half's results leave as partials of their own: [rows, NP], NP = 2
-// per vocab tile.  One 4 KB staging buffer a warp (as in epilogues.cuh) keeps
-// the operand stages' room.
+// columns) of the tile, so that two warps take turns on each SM quarter's
+// special-function unit and hide each other's waits (a step of 1531 x 1024 x
+// 50257: 498 us with four warps, 476 with eight).  What bounds a logits GEMM:
+// the tensor cores from H = 512 on, below that this epilogue -- 4096 x 256 x 50257
+// takes 109 us against 46 for its products and 61 for the main loop alone.  The
+// half's results leave as partials of their own: [rows, NP], NP = 2 per vocab
+// tile.  One 4 KB staging buffer a warp (as in epilogues.cuh) keeps the operand
+// stages' room.
 
 // Waits until the warp's staging buffer is no longer read by its last store.
 __device__ __forceinline__ void stage_reuse(int lane) {
@@ -835,7 +836,8 @@ __device__ __forceinline__ CeMerged ce_merge_row(const float2* __restrict__ pr,
 // Merges the tile partials of each row into its LSE and row loss.  All rows of
 // the chunk's part of the list write the caller's row loss and LSE (0 for
 // left-out rows) and their share k_r l_r of the loss (list order); lse2 (if
-// given) is for the recompute GEMM.  One warp per row, or, when the rows are too few to fill the SMs so, one block.
+// given) is for the recompute GEMM.  One warp per row, or, when the rows are too
+// few to fill the SMs so, one block.
 template <bool kBlockRow>
 __global__ void __launch_bounds__(256)
     k_ce_merge(const float2* __restrict__ partials, const float* __restrict__ zsum, int NP,
@@ -843,8 +845,8 @@ __global__ void __launch_bounds__(256)
                const int32_t* __restrict__ list, const float* __restrict__ zlab,
                const float* __restrict__ kw, float* __restrict__ lse2,
                float* __restrict__ row_loss, float* __restrict__ lse_out,
-               float* __restrict__ share, const float* __restrict__ all_shares, long long N, DeviceCtl* ctl, unsigned blocks,
-               float* __restrict__ loss) {
+               float* __restrict__ share, const float* __restrict__ all_shares, long long N,
+               DeviceCtl* ctl, unsigned blocks, float* __restrict__ loss) {
   pdl_wait();
   pdl_trigger();
   const int row = kBlockRow ? blockIdx.x : blockIdx.x * kCeWarps + (threadIdx.x >> 5);
@@ -875,8 +877,8 @@ __global__ void __launch_bounds__(256)
 // stored exponentials, in place: fp16 E -> bf16 G = kap E 2^(m_t - L2) - targets,
 // rounded once; the label's entry, which E leaves out, from q_y - 1.  A row takes a
 // warp (small vocabularies) or gridDim.y blocks (each merges the partials for
-// itself), 16 bytes a thread at a time, four loads ahead.  Bound by HBM: 4 bytes per entry; 4096 x 128256 in 362
-// us, 5.8 TB/s (384 with the registers of 3 blocks an SM instead of 4).
+// itself), 16 bytes a thread at a time, four loads ahead.  Bound by HBM: 4 bytes
+// per entry; 4096 x 128256 in 362 us, 5.8 TB/s (384 with the registers of 3 blocks an SM instead of 4).
 template <bool kBlockRow>
 __global__ void __launch_bounds__(256, 4)
     k_ce_dlogits(const float2* __restrict__ partials, const float* __restrict__ zsum, int NP,

@@ -228,7 +228,8 @@ fckl_status fckl_block_norm_bwd(const fckl_norm_problem* prob, const void* x, co
   const double xs = xb ? 2.0 : 4.0, n = (double)prob->N * prob->H;
   {
     ProfScope ps(K_NORM_BWD, st, 30.0 * n,
-                 n * (xs + (block ? 2.0 : 0.0) + (dy ? (prob->dy_type == FCKL_BFLOAT ? 2.0 : 4.0) : 0.0) +
+                 n * (xs + (block ? 2.0 : 0.0) +
+                      (dy ? (prob->dy_type == FCKL_BFLOAT ? 2.0 : 4.0) : 0.0) +
                       (dv ? xs : 0.0) + (dx ? xs : 0.0) + (dblock ? 2.0 : 0.0)));
     FCKL_LAUNCH(k, grid, s.threads, smem, a);
   }

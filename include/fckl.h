@@ -358,7 +358,8 @@ fckl_status fckl_ce_fwd(const fckl_ce_problem* prob, const void* hidden, const v
  * grad_type, overwritten.  row_loss and lse may be NULL, and so may one of dH
  * and dW (a frozen projection, or frozen rows: that product is not computed).
  * 6*H*V flops per kept row: the forward keeps one chunk's exponentials in the
- * block that dlogits then takes, so nothing is computed twice. */
+ * block that dlogits then takes (8*H*V for short hidden rows, H <= 384, against
+ * large vocabularies, where computing the logits again costs less). */
 fckl_status fckl_ce_fwd_bwd(const fckl_ce_problem* prob, const void* hidden, const void* W,
                             const void* labels, const float* row_weight, float* loss,
                             float* row_loss, float* lse, void* dH, void* dW, void* workspace,

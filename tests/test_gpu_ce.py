@@ -535,6 +535,7 @@ def test_host_threads_on_their_own_streams():
     (1400, 64, 48000, {}),                                  # logits computed twice
     (1400, 64, 48000, dict(label_smoothing=0.1, z_loss=1e-3)),
     (2900, 40, 48001, dict(chunk=1450)),                    # the same in chunks
+    (1000, 40, 70000, {}),                                  # and selected in one launch
     (1300, 72, 700, {}), (1300, 72, 8192, {}),              # a warp a row of dlogits
     (1184, 72, 700, {}), (1300, 72, 8200, {})])             # just past those
 def test_both_sides_of_every_rule(N, H, V, kw):
