@@ -1,7 +1,7 @@
 // Host side of the vocabulary cross entropy: checks, workspace layout and the
 // chunk loop.  Per chunk of C kept rows, on the caller's stream:
-//   gather rows -> logits GEMM (log-sum-exp epilogue) -> merge (row losses; the
-//   last block adds up the loss),
+//   gather rows -> logits GEMM (log-sum-exp epilogue), or W streamed past one or
+//   two rows -> merge (row losses; the last block adds up the loss),
 // with gradients
 //   gather rows -> logits GEMM (and its exponentials) -> merge and dlogits, or,
 //   for given log-sum-exps, gather rows -> logits GEMM (dlogits epilogue),
@@ -85,6 +85,18 @@ long long ce_rows(const fckl_ce_problem* p) {
   return std::min<long long>(p->N, (long long)align_up((size_t)cdiv(p->N, chunks), 128));
 }
 
+// Scoring calls of one or two rows stream W past them instead of multiplying
+// tiles of 256 rows, whose products alone take 157 us at 4096 x 128256 (bytes: 163).
+// Graph-timed, us, tiles and streamed: one row 4096 x 128256 184 and 157, 2048 x 32000
+// 38 and 28, 1344 x 583 19 and 10; two rows of 4096 x 128256 184 and 170.  Four rows
+// (184 and 188) and eight (184 and 373) are bound by the sums' arithmetic.
+bool ce_few(long long C) { return C <= kFewRows; }
+
+template <int kRows, int kAhead>
+auto ce_few_kernel(bool smooth) {
+  return smooth ? k_ce_few<kRows, kAhead, true> : k_ce_few<kRows, kAhead, false>;
+}
+
 CeLayout ce_layout(const fckl_ce_problem* p, bool grads) {
   CeLayout L{};
   L.C = ce_rows(p);
@@ -104,8 +116,9 @@ CeLayout ce_layout(const fckl_ce_problem* p, bool grads) {
   L.off_zlab = take(C * 4);
   L.off_lse2 = take(C * 4);
   L.off_rest = take(C * 4);
-  L.off_part = take(C * 2 * L.NT * sizeof(float2));
-  L.off_zsum = take(p->label_smoothing > 0.f ? C * 2 * L.NT * 4 : 0);
+  const size_t NP = (size_t)std::max(2 * L.NT, ce_few(L.C) ? cdiv(p->V, kFewCols) : 0);
+  L.off_part = take(C * NP * sizeof(float2));
+  L.off_zsum = take(p->label_smoothing > 0.f ? C * NP * 4 : 0);
   L.off_h = take(align_up(C, CM) * p->H * 2);
   L.off_dlog = take(grads ? C * L.Vp * 2 : 0);
   // S segments of MT row tiles fit when S * MT * NTh <= slab_units
@@ -324,7 +337,15 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
   FCKL_LAUNCH((gemm_pair_kernel<Epi, false, false>), Gv, gemm_threads<Epi>(), \
               pair_smem_bytes<Epi>(), mapH_k, mapW_k, map, params, sa_v, ca)
     if (q.mode == CeMode::kFwd || recompute) {
-      {
+      const bool few = q.mode == CeMode::kFwd && ce_few(L.C);
+      const int NPm = few ? (int)cdiv(V, kFewCols) : NP;
+      if (few) {
+        ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + nr * NPm * 8.0);
+        auto few_kernel = cap == 1 ? ce_few_kernel<1, 2>(smooth) : ce_few_kernel<2, 4>(smooth);
+        FCKL_LAUNCH(few_kernel, (int)cdiv(V, kFewCols), 256, 0, rc, cap, H, V, NPm,
+                    (float)(1.4426950408889634 / prob->T), (const __nv_bfloat16*)hst,
+                    static_cast<const __nv_bfloat16*>(q.W), (const int*)lab, part, zsum);
+      } else {
         ProfScope ps(K_CE_FWD, st, flops, 2.0 * (nr + V) * H + nr * NT * 8.0);
         if (smooth) {
           EpiCe<true>::Params pf{V, NP, scale2, lab, part, zsum};
@@ -337,7 +358,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
       ProfScope ps(K_MERGE, st, 0.0, nr * (NT * 8.0 + 28.0));
       const bool block_row = ce_block_rows(cap);
       FCKL_LAUNCH(block_row ? k_ce_merge<true> : k_ce_merge<false>,
-                  block_row ? cap : (int)cdiv(cap, kCeWarps), 256, 0, (const float2*)part, zs, NP,
+                  block_row ? cap : (int)cdiv(cap, kCeWarps), 256, 0, (const float2*)part, zs, NPm,
                   rc, cap, V, invT, prob->label_smoothing, prob->z_loss, clist, (const float*)zlab,
                   (const float*)kw, recompute ? lse2 : nullptr, q.row_loss, q.lse_out, share + row0,
                   (const float*)share, N, ctl, blocks, q.loss);

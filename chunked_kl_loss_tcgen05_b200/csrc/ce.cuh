@@ -246,6 +246,100 @@ __global__ void __launch_bounds__(128)
   if (threadIdx.x == 0) zlab[i] = z;
 }
 
+// ---------------------------------------------------------------- few rows
+constexpr int kFewCols = 32;  // vocabulary columns per block of k_ce_few
+constexpr int kFewRows = 2;   // rows of a chunk that take it
+
+// 16 bytes that are read once: not kept in L1.
+__device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Forward of up to kRows rows: what EpiCe leaves, per 32 columns instead of 128.
+// W is streamed once, a warp taking four of its rows at a time with kAhead
+// 16-byte vectors of each on their way; the hidden rows come from L1.  The sums
+// are fp32 products in pairs, so nothing is cut and scale2 is the plain log2(e) / T.
+// W does not depend on the kernel ahead (which selects the rows): its first loads
+// do not wait for it.  Bound by HBM: 4096 x 128256 in 153 us, 6.9 TB/s.  kAhead = 1, 2,
+// 4: one row 162, 157, 159 us, two rows 175, 184, 170.
+template <int kRows, int kAhead, bool kSum>
+__global__ void __launch_bounds__(256)
+    k_ce_few(RowCount rc, int cap, int H, int V, int NP, float scale2,
+             const __nv_bfloat16* __restrict__ hst, const __nv_bfloat16* __restrict__ W,
+             const int* __restrict__ lab, float2* __restrict__ partials,
+             float* __restrict__ zsum) {
+  constexpr int kCols = kFewCols / 8;
+  __shared__ float z_sh[kRows][kFewCols];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = blockIdx.x * kFewCols, nv = H / 8;
+  const __nv_bfloat16* wr[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c)
+    wr[c] = W + (size_t)min((long long)n0 + warp * kCols + c, (long long)V - 1) * H;
+  uint4 w[kAhead][kCols];
+  auto fetch = [&](int u, int j) {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+      w[u][c] = j < nv ? load_once(wr[c] + 8 * (size_t)j) : make_uint4(0u, 0u, 0u, 0u);
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) fetch(u, 32 * u + lane);
+  pdl_wait();
+  pdl_trigger();
+  const int n = rc.get();
+  if (n <= 0) return;
+  float2 acc[kCols][kRows];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c)
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) acc[c][r] = both(0.f);
+  for (int j0 = lane; j0 - lane < nv; j0 += 32 * kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = j0 + 32 * u;
+      float2 x[kCols][4];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) Raw8<__nv_bfloat16>{w[u][c]}.get(x[c]);
+      fetch(u, j + 32 * kAhead);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        Raw8<__nv_bfloat16> h{make_uint4(0u, 0u, 0u, 0u)};
+        if (j < nv) h.load(hst + (size_t)min(r, cap - 1) * H + 8 * (size_t)j);
+        float2 y[4];
+        h.get(y);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[c][r] = fma2(x[c][k], y[k], acc[c][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      const float t = warp_sum(acc[c][r].x + acc[c][r].y);
+      if (lane == 0) z_sh[r][warp * kCols + c] = t;
+    }
+  __syncthreads();
+  if (warp >= kRows || warp >= n) return;
+  const long long col = (long long)n0 + lane;
+  const float z = z_sh[warp][lane];
+  const bool in = col < V, counts = in && col != lab[warp];  // the label's column is left out
+  const float m = warp_max(counts ? z * scale2 : -INFINITY);
+  const float ref = m == -INFINITY ? 0.f : m;
+  const float s = warp_sum(counts ? ex2_approx(fmaf(z, scale2, -ref)) : 0.f);
+  const float u = kSum ? warp_sum(in ? z : 0.f) : 0.f;
+  if (lane == 0) {
+    partials[(size_t)warp * NP + blockIdx.x] = make_float2(m, s);
+    if (kSum) zsum[(size_t)warp * NP + blockIdx.x] = u;
+  }
+}
+
 // ---------------------------------------------------------------- epilogues
 // All with eight warps: a thread owns one accumulator row and one half (128
 // columns) of the tile, so that two warps take turns on each SM quarter's
@@ -878,7 +972,8 @@ __global__ void __launch_bounds__(256)
 // rounded once; the label's entry, which E leaves out, from q_y - 1.  A row takes a
 // warp (small vocabularies) or gridDim.y blocks (each merges the partials for
 // itself), 16 bytes a thread at a time, four loads ahead.  Bound by HBM: 4 bytes
-// per entry; 4096 x 128256 in 362 us, 5.8 TB/s (384 with the registers of 3 blocks an SM instead of 4).
+// per entry; 4096 x 128256 in 362 us, 5.8 TB/s (384 with the registers of 3 blocks
+// an SM instead of 4).
 template <bool kBlockRow>
 __global__ void __launch_bounds__(256, 4)
     k_ce_dlogits(const float2* __restrict__ partials, const float* __restrict__ zsum, int NP,

@@ -547,3 +547,47 @@ def test_both_sides_of_every_rule(N, H, V, kw):
     check_grads(c, o, dH, dW)
     again = fused_ce_fwd_bwd(c.hidden, c.W, c.labels, row_weight=c.weight, **kw)
     assert torch.equal(dH, again[2]) and torch.equal(dW, again[3])
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(T=0.7, label_smoothing=0.2, z_loss=1e-3)])
+@pytest.mark.parametrize("N,H,V,chunk", [
+    (1, 8, 1, 0), (1, 8, 31, 0), (2, 40, 33, 0),
+    (1, 256, 1003, 0), (1, 264, 64, 0), (2, 1024, 777, 0), (2, 1032, 97, 0),
+    (1, 4104, 2050, 0), (2, 4104, 2050, 0),
+    (5, 136, 300, 1), (5, 136, 300, 2),
+])
+def test_few_rows_are_streamed(N, H, V, chunk, kw):
+    c = Case(N, H, V, seed=11, ignored=0.0, lift=1.0)
+    loss, row_loss, lse = fused_ce_fwd(c.hidden, c.W, c.labels, chunk=chunk, **kw)
+    check_losses(c, c.oracle(**kw), loss, row_loss, lse, T=kw.get("T", 1.0),
+                 z_loss=kw.get("z_loss", 0.0))
+
+
+@pytest.mark.parametrize("left_out", [(0,), (1,), (0, 1)])
+def test_few_rows_with_some_left_out(left_out):
+    c = Case(2, 72, 130, seed=3, ignored=0.0)
+    hidden = c.hidden.clone()
+    for r in left_out:
+        c.y[r] = -100
+        hidden[r] = float("nan")
+    labels = torch.from_numpy(c.y).cuda()
+    loss, row_loss, lse = fused_ce_fwd(hidden, c.W, labels)
+    check_losses(c, c.oracle(), loss, row_loss, lse)
+
+
+def test_few_rows_with_infinities():
+    # an infinite logit apart from the label's: the row's loss is no number, or
+    # infinite; minus infinity: the column has no share
+    c = Case(2, 64, 100, seed=4, ignored=0.0)
+    W = c.W.clone()
+    hidden = c.hidden.clone()
+    hidden[:, 0] = torch.tensor([-1.0, 1.0])
+    W[:, 0] = 0
+    at = next(v for v in range(c.V) if v not in c.y)
+    W[at, 0] = float("inf")
+    _, row_loss, _ = fused_ce_fwd(hidden, W, c.labels)
+    z = hidden[0].double() @ torch.where(W.isinf(), 0, W).double().T
+    z[at] = -float("inf")
+    want = (torch.logsumexp(z, 0) - z[c.y[0]]).item()
+    assert abs(row_loss[0].item() - want) <= 2 * c.dz(1.0) + 8 * 2.0 ** -22 * (1 + abs(want))
+    assert not np.isfinite(row_loss[1].item())
