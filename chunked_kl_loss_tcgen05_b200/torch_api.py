@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import dataclasses
 import functools
+from operator import index as _int
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -427,6 +428,8 @@ def _placed(index, tensors):
     return index >= 0
 
 
+# The caches below are keyed by plain numbers: a tensor would be remembered by its
+# identity, and its later values never seen.  So options become float / int first.
 @functools.lru_cache(maxsize=256)
 def _ce_problem(*fields):
     """The problem of these sizes and options, and its workspace sizes without and
@@ -469,9 +472,10 @@ def _ce_setup(hidden, W, labels, rows, T, label_smoothing, z_loss, ignore_index,
         raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
     if not placed:
         _check_placement(True, [("hidden", hidden), ("W", W), ("labels", labels)] + list(rows))
-    prob, *nbytes = _ce_problem(N, H, W.shape[0], T, label_smoothing, z_loss,
-                                _REDUCTIONS[reduction], ignore_index, chunk, n_valid_total,
-                                _LABEL_TYPES[labels.dtype], _GRAD_TYPES[grad_dtype])
+    prob, *nbytes = _ce_problem(N, H, W.shape[0], float(T), float(label_smoothing), float(z_loss),
+                                _REDUCTIONS[reduction], _int(ignore_index), _int(chunk),
+                                _int(n_valid_total), _LABEL_TYPES[labels.dtype],
+                                _GRAD_TYPES[grad_dtype])
     if workspace is None:
         if nbytes[gradients] == 0:
             raise FcklError(1, "fckl_ce_workspace_bytes")
@@ -598,6 +602,13 @@ def _scale_gradient(t, factor):
         raise FcklError(st, "fckl_scale_gradient")
 
 
+def _option(name, value):
+    """A differentiable call's option as a number: backward sees what forward saw."""
+    if isinstance(value, torch.Tensor) and value.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} gets no gradient; detach it")
+    return float(value)
+
+
 class FusedCrossEntropy(torch.autograd.Function):
     """Cross entropy with gradients for hidden and W, in their own dtype (bf16).
 
@@ -672,11 +683,12 @@ def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_sm
         raise ValueError(f'reduction must be "mean", "sum" or "none", got {reduction!r}')
     if norm is not None:
         hidden = norm(hidden)
-    opts = dict(T=T, label_smoothing=label_smoothing, z_loss=z_loss, chunk=chunk)
+    opts = dict(T=_option("T", T), label_smoothing=_option("label_smoothing", label_smoothing),
+                z_loss=_option("z_loss", z_loss), chunk=_int(chunk))
     if not torch.is_grad_enabled():  # (inside a Function's forward this cannot be told)
         hidden, W = hidden.detach(), W.detach()
-    return FusedCrossEntropy.apply(hidden, W, labels, row_weight, reduction, ignore_index, check,
-                                   opts)
+    return FusedCrossEntropy.apply(hidden, W, labels, row_weight, reduction, _int(ignore_index),
+                                   check, opts)
 
 
 # ---------------------------------------------------------------- norms around a block
@@ -728,7 +740,7 @@ def _norm_problem(x, block, post_weight, gate, pre_weight, scale, post, pre, eps
               and _placed(index, (x, block, post_weight, gate, pre_weight, dy, dv)))
     if not ok:
         _norm_checks(x, block, post_weight, gate, pre_weight, dy, dv)
-    return (shape[0], shape[1], scale, eps, weight_offset,
+    return (shape[0], shape[1], float(scale), float(eps), float(weight_offset),
             (FCKL_NORM_POST if post else 0) | (FCKL_NORM_PRE if pre else 0),
             _REAL_TYPES[x.dtype], _REAL_TYPES[wt] if wt else FCKL_FLOAT,
             FCKL_BFLOAT if dy is None else _REAL_TYPES[dy.dtype])
@@ -855,8 +867,9 @@ def block_norm(x, block=None, post_weight=None, gate=None, pre_weight=None, scal
     """Differentiable block_norm_fwd: (v, y)."""
     if block is None and not pre:
         raise ValueError("without a block there must be a pre-norm")
-    opts = dict(scale=scale, post=post_weight is not None if post is None else bool(post),
-                pre=bool(pre), eps=eps, weight_offset=weight_offset)
+    opts = dict(scale=_option("scale", scale),
+                post=post_weight is not None if post is None else bool(post), pre=bool(pre),
+                eps=_option("eps", eps), weight_offset=_option("weight_offset", weight_offset))
     out = BlockNorm.apply(x, block, post_weight, gate, pre_weight, opts)
     if block is None:
         return x, out
