@@ -869,22 +869,25 @@ __device__ __forceinline__ void ce_finish_loss(const float* share, long long N, 
 }
 
 // A row from its merged partials over the columns but the label: S 2^M (base 2),
-// the label's exponent a2 = z_y log2(e) / T, and the mean of a_v (smoothing).
+// the label's exponent a2 = z_y log2(e) / T, and the mean of a_v (smoothing).  The
+// LSE is formed from the larger side: from a label far below the others it would
+// take over ulp(a_y), 6e-5 at a_y = -1000, and no number at -inf, where only the
+// loss is infinite.
 struct CeRow {
   float L2, lse, nll, loss, q1;  // log2(e) LSE, LSE, LSE - a_y, l_r, q_y - 1
   __device__ __forceinline__ CeRow(float M, float S, float a2, float mean, float smooth,
                                    float zloss) {
-    const float x = (M - a2) + log2f(S);  // log2 R; -inf when the label is alone
+    const float t = M + log2f(S), x = t - a2;  // log2 R; -inf when the label is alone
     // beyond 2^24 the 1 in 1 + R is below R's last bit
     const float R = exp2f(x);
     nll = x > 24.f ? x * kLn2 : log1pf(R);
     if (!(a2 < INFINITY)) nll = NAN;  // an overflowed label logit is no certainty
     q1 = x > 24.f ? exp2f(-x) - 1.f : -R / (1.f + R);
-    lse = fmaf(a2, kLn2, nll);
-    L2 = fmaf(nll, kLog2e, a2);
-    loss = nll;
-    if (smooth > 0.f) loss += smooth * ((lse - mean) - nll);
-    loss = fmaf(zloss * lse, lse, loss);
+    const float big = x > 0.f ? t : a2, more = x > 0.f ? log1pf(exp2f(-x)) : nll;
+    lse = fmaf(big, kLn2, more);
+    L2 = fmaf(more, kLog2e, big);
+    loss = smooth > 0.f ? fmaf(1.f - smooth, nll, smooth * (lse - mean)) : nll;
+    if (zloss > 0.f) loss = fmaf(zloss * lse, lse, loss);
   }
 };
 

@@ -1,0 +1,91 @@
+"""Cross entropy rows whose label lies far below the other columns, or at minus
+infinity, against the fp64 oracle.
+
+Logits are exact here (one nonzero hidden value a row, or sums of few terms), so a
+log-sum-exp is off only by its own arithmetic: the exponent of each column
+(relative 2^-24 of at most 2^5), ex2 (2^-22) and a few fp32 roundings of values up
+to |LSE| + 1: 8 2^-22 (1 + |LSE|).  A row loss adds 2^-22 of itself.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from chunked_kl_loss_tcgen05_b200.torch_api import fused_ce_bwd, fused_ce_fwd, fused_ce_fwd_bwd
+
+pytestmark = pytest.mark.gpu
+BF16, FP16 = 2.0 ** -8, 2.0 ** -11
+
+
+def device(bits):
+    return torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16)
+
+
+@pytest.mark.parametrize("N,V", [(1, 300), (2, 300), (40, 300), (40, 5000)])
+def test_label_far_below_the_others(N, V):
+    """z = h_0 W_v0 exactly: other columns between -4 and 4, the labels between
+    -100 and -3400."""
+    rng = np.random.default_rng(N + V)
+    H = 8
+    h, W = np.zeros((N, H), np.float32), np.zeros((V, H), np.float32)
+    h[:, 0] = 1
+    W[:, 0] = rng.integers(-16, 17, V) / 4
+    y = rng.permutation(V)[:N]
+    h[:, 1] = rng.integers(100, 256, N) / 8       # hits only the labels' rows of W
+    W[y, 1] = -rng.integers(8, 108, N).astype(np.float32)
+    hb, Wb = synth.f32_to_bf16_bits(h), synth.f32_to_bf16_bits(W)
+    o = oracle.cross_entropy(hb, Wb, y)
+    labels = torch.from_numpy(y).cuda()
+    runs = [fused_ce_fwd(device(hb), device(Wb), labels)[1:]]
+    runs.append((fused_ce_fwd_bwd(device(hb), device(Wb), labels)[1], None))
+    tol = 8 * 2.0 ** -22 * (1 + np.abs(o["lse"]))
+    for rows, lse in runs:
+        err = np.abs(rows.cpu().numpy() - o["row_loss"])
+        assert (err <= tol + 2.0 ** -21 * o["row_loss"]).all(), err.max()
+        if lse is not None:
+            err = np.abs(lse.cpu().numpy() - o["lse"])
+            assert (err <= tol).all(), (err.max(), tol.max())
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(label_smoothing=0.1, z_loss=1e-3)])
+@pytest.mark.parametrize("N,H,V,at", [
+    (1, 64, 300, 0), (2, 64, 300, 1), (50, 64, 300, 7), (1300, 64, 700, 1200),
+    (1400, 64, 48000, 7)])                       # streamed, in a block, a warp a row, recomputed
+def test_label_at_minus_infinity(N, H, V, at, kw):
+    """h . W_y overflows to -inf for one row: its loss is infinite, its log-sum-exp
+    and all gradients are what they are without that column."""
+    rng = np.random.default_rng(N + V)
+    h = rng.standard_normal((N, H)).astype(np.float32)
+    W = (rng.standard_normal((V, H)) * 0.1).astype(np.float32)
+    A = float((np.abs(h[:64]) @ np.abs(W[:4096]).T).max()) * 1.5
+    y = rng.integers(0, V, N)
+    h[:, 0], W[:, 0] = 0, 0
+    h[at, 0], W[y[at], 0] = 2.0 ** 100, -2.0 ** 100
+    hb, Wb = synth.f32_to_bf16_bits(h), synth.f32_to_bf16_bits(W)
+    o = oracle.cross_entropy(hb, Wb, y, **kw)
+    g = rng.standard_normal(N).astype(np.float32)
+    og = oracle.cross_entropy(hb, Wb, y, row_grad=g, **kw)
+    hd, Wd, labels = device(hb), device(Wb), torch.from_numpy(y).cuda()
+    dz = H * 2.0 ** -23 * A
+    tol = (2 * dz + 8 * 2.0 ** -22 * (1 + np.abs(o["lse"]).max())) * 1.1
+    rest = np.arange(N) != at
+    loss, rows, lse = fused_ce_fwd(hd, Wd, labels, **kw)
+    both = fused_ce_fwd_bwd(hd, Wd, labels, **kw)
+    assert np.abs(lse.cpu().numpy() - o["lse"]).max() <= tol
+    for r in (rows, both[1]):
+        r = r.cpu().numpy()
+        assert r[at] == np.inf
+        assert (np.abs(r - o["row_loss"])[rest] <= tol).all()
+    assert loss.item() == np.inf and both[0].item() == np.inf
+    grads = fused_ce_bwd(hd, Wd, labels, lse, torch.from_numpy(g).cuda(), **kw)
+    for ref, pair in ((o, both[2:]), (og, grads)):
+        for name, t in zip(("dH", "dW"), pair):
+            # dlogits' rounding; and of q = G + e / V, to which a smoothed G can be
+            # small (q near e / V), the 16-bit exponential's, the logits' error and
+            # the fp32 exponent's (z/T - LSE) few 2^-20
+            err = np.abs(t.double().cpu().numpy() - ref[name])
+            bound = (1.05 * (BF16 + 2 * dz + 2.0 ** -20) * ref[name + "_abs"]
+                     + 2.0 ** -22 * np.abs(ref[name]) + 1e-30
+                     + 1.05 * (FP16 + 2 * dz + 2.0 ** -18) * ref[name + "_q"])
+            assert (err <= bound).all(), (name, (err / bound).max())
