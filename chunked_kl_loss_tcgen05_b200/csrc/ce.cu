@@ -33,13 +33,21 @@ constexpr int kPollNs = 30;
 // The scale that the epilogues multiply the logits with makes up for 0.14 of it.
 constexpr double kCutShare = 0.14;
 
-// Calls of up to this many rows run their dH GEMM (which reads W) and their dW
-// GEMM (which writes as much) side by side, on 3/8 and 5/8 of the CTA pairs: both
-// wait for memory most of the time.  Graph-timed steps, us, one after the other
-// and side by side: 1 x 1024 x 32000 75 and 66, 128 x 4096 x 128256 757 and 706,
-// 200 x 2048 x 32000 142 and 130, 256 x 256 x 4096 33.4 and 30.7; from 256 rows
-// on (256 x 4096 x 128256: 846 and 855) the tensor cores start to limit both.
-constexpr int kTwoRows = 256;
+// Calls of one row tile run their dH GEMM (which reads W) and their dW GEMM (which
+// writes as much) side by side, on 3/8 and 5/8 of the CTA pairs, unless W is large:
+// small ones are bound by launches and tails, large ones by what an SM can store, and
+// there dW needs all of them.  More rows carry it further with bf16 gradients, where
+// the products grow and dW's bytes do not; fp32 ones cost more when dH goes first.
+// Graph-timed steps with L2 flushed, us, one after the other and side by side; bf16
+// gradients: 256 x 256 x 4096 37 and 35, 16 x 512 x 32000 55 and 51, 256 x 1024 x 32000 96
+// and 86, 16 x 2880 x 8192 66 and 70, 64 x 1024 x 50257 96 and 107, 128 x 4096 x 128256
+// 721 and 862; fp32: 64 x 1024 x 50257 119 and 115, 64 x 2048 x 32000 both 137, 128 x 4096 x
+// 128256 919 and 1001.  Two row tiles: 384 x 2880 x 8192 92 and 98.
+constexpr int kTwoRows = PM;
+bool ce_two(long long rows, long long V, long long H, bool bf16_grads) {
+  if (rows > kTwoRows) return false;
+  return V * H <= (bf16_grads ? (1ll << 24) + rows * (1ll << 17) : 1ll << 26);
+}
 
 // Room for the k segments of a chunk's dH GEMM: four units for every CTA pair
 // of a B200 (more would mean more slabs to sum than waves to balance), 256 KB
@@ -415,7 +423,7 @@ fckl_status enqueue_ce(const CeRequest& q, const CeLayout& L, const CeDevice* de
                                   bf16_grads ? static_cast<__nv_bfloat16*>(q.dW) : nullptr};
     const double dh_bytes = 2.0 * nr * V + 2.0 * (double)V * H + 4.0 * nr * H;
     const double dw_bytes = 2.0 * nr * (V + H) + (dw_direct16 ? 2.0 : c > 0 ? 8.0 : 4.0) * V * H;
-    const bool two = q.dH && q.dW && L.nchunks == 1 && cap <= kTwoRows;
+    const bool two = q.dH && q.dW && L.nchunks == 1 && ce_two(cap, V, H, bf16_grads);
     const int dh_pairs = two ? std::max(1, pairs * 3 / 8) : pairs;
     if (two) {
       ProfScope ps(K_DHW, st, 2.0 * flops, dh_bytes + dw_bytes);

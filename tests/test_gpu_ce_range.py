@@ -1,10 +1,11 @@
 """Cross entropy rows whose label lies far below the other columns, or at minus
-infinity, against the fp64 oracle.
+infinity, against the fp64 oracle; and the sizes at which calls change their way.
 
-Logits are exact here (one nonzero hidden value a row, or sums of few terms), so a
+Far labels: logits are exact here (one nonzero hidden value a row, or sums of few terms), so a
 log-sum-exp is off only by its own arithmetic: the exponent of each column
 (relative 2^-24 of at most 2^5), ex2 (2^-22) and a few fp32 roundings of values up
-to |LSE| + 1: 8 2^-22 (1 + |LSE|).  A row loss adds 2^-22 of itself.
+to |LSE| + 1: 8 2^-22 (1 + |LSE|).  A row loss adds five roundings of
+2^-24 of itself (log2 e and its product, the difference, ln 2 and its product): 2^-21.
 """
 import numpy as np
 import pytest
@@ -12,6 +13,7 @@ import torch
 
 import oracle
 import synth
+from chunked_kl_loss_tcgen05_b200 import fckl_profile_begin, fckl_profile_end
 from chunked_kl_loss_tcgen05_b200.torch_api import fused_ce_bwd, fused_ce_fwd, fused_ce_fwd_bwd
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +91,31 @@ def test_label_at_minus_infinity(N, H, V, at, kw):
                      + 2.0 ** -22 * np.abs(ref[name]) + 1e-30
                      + 1.05 * (FP16 + 2 * dz + 2.0 ** -18) * ref[name + "_q"])
             assert (err <= bound).all(), (name, (err / bound).max())
+
+
+@pytest.mark.parametrize("N,H,V,dtype,side_by_side", [
+    (8, 256, 65000, torch.bfloat16, True), (8, 256, 70000, torch.bfloat16, False),
+    (256, 256, 70000, torch.bfloat16, True), (257, 64, 1000, torch.bfloat16, False),
+    (256, 64, 1000, torch.float32, True), (8, 256, 262144, torch.float32, True),
+    (8, 256, 262145, torch.float32, False), (256, 4096, 128256, torch.bfloat16, False)])
+def test_gradient_products_side_by_side(N, H, V, dtype, side_by_side):
+    """Which calls run dH and dW in one launch, and that both ways give the gradients
+    that the dW of one-row-tile chunks, in launches of their own, adds up to."""
+    g = torch.Generator(device="cuda").manual_seed(N + V)
+    h = torch.randn(N, H, generator=g, device="cuda").bfloat16()
+    W = torch.empty(V, H, dtype=torch.bfloat16, device="cuda").normal_(0, 0.05, generator=g)
+    y = torch.randint(0, V, (N,), generator=g, device="cuda")
+    fckl_profile_begin()
+    _, _, dH, dW = fused_ce_fwd_bwd(h, W, y, grad_dtype=dtype, check=False)
+    kinds = {k["name"] for k in fckl_profile_end()}
+    assert ("dH_dW_gemm" in kinds) == side_by_side
+    assert bool(kinds & {"dH_gemm", "dW_gemm"}) != side_by_side
+    _, _, rH, rW = fused_ce_fwd_bwd(h, W, y, chunk=N // 2 + 1, check=False)
+    for t, r in ((dH, rH), (dW, rW)):
+        # the same bf16 dlogits; fp32 sums in another order (the tensor cores cut a
+        # segment's sum at most 2100 times here, 0.18 2^-23 of it each on average)
+        # and, in bf16, one rounding
+        own = BF16 if dtype == torch.bfloat16 else 0.0
+        e = (t.float() - r).abs()
+        assert (e <= own * r.abs() + 2.0 ** -10 * r.abs().max()).all()
+        assert (e.double().norm() <= (own / 2 + 2.0 ** -14) * r.double().norm()).item()
