@@ -51,7 +51,8 @@ bool ce_two(long long rows, long long V, long long H, bool bf16_grads) {
 
 // Room for the k segments of a chunk's dH GEMM: four units for every CTA pair
 // of a B200 (more would mean more slabs to sum than waves to balance), 256 KB
-// each, or one segment of every tile.
+// each, or one segment of every tile; and no more than the GEMM can choose, which
+// has a k-block of the vocabulary at least in a segment and at most 128 segments.
 constexpr int kSlabUnits = 4 * 74;
 
 enum class CeMode { kFwd, kFwdBwd, kBwd };
@@ -113,7 +114,9 @@ CeLayout ce_layout(const fckl_ce_problem* p, bool grads) {
   L.NTh = cdiv(p->H, BN);
   L.nchunks = cdiv(p->N, L.C);
   const long long tiles = cdiv(L.C, PM) * L.NTh;
-  L.slab_units = (int)std::min<long long>(std::max<long long>(tiles, kSlabUnits), INT32_MAX);
+  const long long segments = std::min<long long>(cdiv(p->V, BK), kMaxSplit);
+  L.slab_units = (int)std::min<long long>(
+      {std::max<long long>(tiles, kSlabUnits), tiles * segments, INT32_MAX});
   size_t off = align_up(sizeof(DeviceCtl), kAlign);
   auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, kAlign); return o; };
   const size_t C = (size_t)L.C;

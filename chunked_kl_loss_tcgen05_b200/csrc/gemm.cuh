@@ -46,6 +46,7 @@ constexpr int PM = 256;  // rows of a pair tile
 constexpr int CM = 128;  // rows per CTA
 constexpr int BN = 256;  // columns of a tile
 constexpr int BK = 64;   // k-block
+constexpr int kMaxSplit = 128;  // k segments chosen on the device
 constexpr uint32_t A_HALF_BYTES = CM * BK * 2;        // 16 KB
 constexpr uint32_t B_HALF_BYTES = (BN / 2) * BK * 2;  // 16 KB
 constexpr uint32_t PSTAGE_BYTES = A_HALF_BYTES + B_HALF_BYTES;
@@ -169,7 +170,7 @@ __device__ __forceinline__ int choose_split_warp(int tiles, int KB, int slots, i
   if (tiles <= 0 || KB <= 0) return 1;
   int best = 1;
   long long best_cost = LLONG_MAX;
-  int smax = KB < 128 ? KB : 128;
+  int smax = min(KB, kMaxSplit);
   if (slab_units > 0) smax = min(smax, max(1, slab_units / tiles));
   for (int S = (threadIdx.x & 31) + 1; S <= smax; S += 32) {
     const int waves = (int)(((long long)tiles * S + slots - 1) / slots);
