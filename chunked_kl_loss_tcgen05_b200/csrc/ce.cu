@@ -81,15 +81,23 @@ bool valid_ce(const fckl_ce_problem* p) {
 bool supported_ce(const fckl_ce_problem* p) { return p->H % 8 == 0; }
 
 // Rows per chunk: the caller's, or the library's automatic rows (resolve_rows)
-// but no fewer than 4096, spread evenly over the nearest number of chunks, so
-// that no chunk is a remainder: every chunk beyond the first reads W twice and
-// reads and writes dW once more.  Measured with bf16 gradients, us per step:
-// 4096 x 2880 x 201088 (2660 kept rows) 10430 at the 2560 rows of 1 GiB, 7900 at
-// 4096; 16384 x 4096 x 128256 43700 at 4096 rows, 45900 at 8192, 49000 at 16384
-// (there the gathered rows no longer stay in L2 beside W).
+// but no fewer than 4096 and no more than 32768, spread evenly over the nearest
+// number of chunks, so that no chunk is a remainder (3/4 to 3/2 of that number,
+// then): every chunk beyond the first reads W twice and reads and writes dW once
+// more.  Measured with bf16 gradients, us per step: 4096 x 2880 x 201088 (2660 kept
+// rows) 10430 at the 2560 rows of 1 GiB, 7900 at 4096; 16384 x 4096 x 128256 43700 at
+// 4096 rows, 45900 at 8192, 49000 at 16384 (there the gathered rows no longer stay in
+// L2 beside W).
+// The upper end is for accuracy: dW sums a chunk's rows on the tensor cores, which
+// cut every partial sum, and a sum of one sign comes out short by 0.7 to 0.8 (rows /
+// 16) 2^-23 of itself; the chunks' sums are rounded.  262144 x 1024 x 1000 (small
+// vocabularies would fit far more rows into 1 GiB): 1.6e-3 short in one chunk, 3490
+// us, 1.8e-4 and 3580 at 32768 rows, 8e-5 and 3730 at 16384.
+constexpr long long kAutoRowsMin = 4096, kAutoRowsMax = 32768;
 long long ce_rows(const fckl_ce_problem* p) {
   if (p->chunk > 0) return std::min<long long>(p->chunk, p->N);
-  const long long want = std::max<long long>(4096, resolve_rows(INT32_MAX, p->V, 0));
+  const long long want =
+      std::clamp<long long>(resolve_rows(INT32_MAX, p->V, 0), kAutoRowsMin, kAutoRowsMax);
   const long long chunks = std::max<long long>(1, (p->N + want / 2) / want);
   return std::min<long long>(p->N, (long long)align_up((size_t)cdiv(p->N, chunks), 128));
 }

@@ -334,9 +334,12 @@ typedef struct {
   float z_loss;          /* lam >= 0                                          */
   int32_t reduction;     /* fckl_reduction                                    */
   int64_t ignore_index;  /* label of rows that do not count                   */
-  int64_t chunk;         /* rows per chunk, 0 = automatic: about as many as
-                            fckl_problem's automatic chunk, at least 4096,
-                            spread evenly                                     */
+  int64_t chunk;         /* rows per chunk; 0 = automatic: the rows whose [rows, V]
+                            block takes 1 GiB, at least 4096 and at most 32768,
+                            spread evenly over the nearest number of chunks (so
+                            3/4 to 3/2 as many, and all N up to 3/2).  dW's
+                            partial sums are cut, not rounded, inside a chunk:
+                            up to about rows / 16 * 1e-7 of a sum of one sign */
   int64_t n_valid_total; /* mean: > 0 replaces the number of kept rows as D   */
   int32_t label_type;    /* fckl_label_type of labels                         */
   int32_t grad_type;     /* fckl_grad_type of dH and dW                       */

@@ -119,3 +119,21 @@ def test_gradient_products_side_by_side(N, H, V, dtype, side_by_side):
         e = (t.float() - r).abs()
         assert (e <= own * r.abs() + 2.0 ** -10 * r.abs().max()).all()
         assert (e.double().norm() <= (own / 2 + 2.0 ** -14) * r.double().norm()).item()
+
+
+@pytest.mark.parametrize("N", [49_151, 200_000])
+def test_long_sums_of_one_sign(N):
+    """dW of classes that no row is labelled with, for positive hidden values: sums of
+    one sign over all rows.  With chunks of at most 49152 rows the tensor cores cut
+    49152 / 16 partial sums, less than 2^-23 of the whole each on average; the bf16
+    rounding of each row's share is random and averages out."""
+    H, V = 64, 64
+    g = torch.Generator(device="cuda").manual_seed(N)
+    h = torch.randn(N, H, generator=g, device="cuda").abs().bfloat16()
+    W = (torch.randn(V, H, generator=g, device="cuda") * 0.02).bfloat16()
+    y = torch.zeros(N, dtype=torch.int64, device="cuda")
+    dW = fused_ce_fwd_bwd(h, W, y)[3].double()
+    q = torch.softmax(h.double() @ W.double().t(), 1)
+    off = (dW / (q.t() @ h.double() / N) - 1)[1:]
+    assert off.mean().abs().item() <= 49152 / 16 * 2.0 ** -23
+    assert off.abs().max().item() <= 49152 / 16 * 2.0 ** -23 + 8 * BF16 / N ** 0.5
