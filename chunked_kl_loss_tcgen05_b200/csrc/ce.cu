@@ -26,11 +26,15 @@ constexpr int kPollNs = 30;
 
 // The tensor cores add 16 products at a time to an fp32 accumulator and cut the
 // sum instead of rounding it, H / 16 times: the logits come out too small in
-// magnitude.  A sum that grows evenly loses (1/2)(mean of ulp(s)/s = 0.72 2^-23)
-// (k / n) of its final value at step k, 0.18 (H / 16) 2^-23 in all; measured, the
-// log-sum-exps fall short by 0.13 to 0.18 (H / 16) 2^-23 of the logits that make
-// them up, for H from 512 to 16384 and logits from 0.2 to 30 (4e-6 at H = 4096).
-// The scale that the epilogues multiply the logits with makes up for 0.14 of it.
+// magnitude, by how much depends on how the sum grows.  In units of (H / 16) 2^-23
+// of the logit, measured for H from 1024 to 16384 and logits from 12 to 30: 0.13 to
+// 0.17 where the products are noise around a mean (what a hidden row and a row of W
+// that it has learned make), 0.25 to 0.67 where all have one sign, nothing where the
+// partial sums are exact (a few nonzero values).  The scale that the epilogues
+// multiply the logits with makes up for 0.14 of it, the first kind, and so leaves a
+// logit off by -0.55 to +0.14 units of itself instead of -0.67 to 0 (one unit is 3e-5
+// at H = 4096).  The label's logit and the streamed rows are rounded sums and not
+// scaled, so a column equal to the label's is off against it by that much.
 constexpr double kCutShare = 0.14;
 
 // Calls of one row tile run their dH GEMM (which reads W) and their dW GEMM (which
