@@ -613,19 +613,22 @@ class FusedCrossEntropy(torch.autograd.Function):
     """Cross entropy with gradients for hidden and W, in their own dtype (bf16).
 
     reduction "mean" / "sum": the fused call computes the gradients in forward;
-    the first backward multiplies them by the upstream factor (rounded once more
-    unless it is a power of two) and hands them over, later ones (retain_graph)
-    compute them again from the saved log-sum-exps.  reduction "none": forward
-    returns the row losses, backward computes the gradients for the given
+    with grad_dtype bfloat16 the first backward multiplies them by the upstream
+    factor (rounded once more unless it is a power of two) and hands them over, and
+    later ones (retain_graph) compute them again from the saved log-sum-exps; with
+    float32 they are kept and rounded once, after the factor.  reduction "none":
+    forward returns the row losses, backward computes the gradients for the given
     upstream gradient."""
 
     @staticmethod
-    def forward(ctx, hidden, W, labels, row_weight, reduction, ignore_index, check, opts):
+    def forward(ctx, hidden, W, labels, row_weight, reduction, ignore_index, check, opts,
+                grad_dtype=torch.bfloat16):
         want = ctx.needs_input_grad[:2]
         ctx.set_materialize_grads(False)
         ctx.reduction, ctx.ignore_index, ctx.check, ctx.opts = reduction, ignore_index, check, opts
         ctx.want, ctx.grads = want, None
         kw = dict(ignore_index=ignore_index, check=check, **opts)
+        ctx.kept = reduction != "none" and any(want) and grad_dtype == torch.float32
         if reduction == "none":
             if row_weight is not None:
                 raise ValueError('row_weight needs reduction "mean" or "sum"')
@@ -633,9 +636,13 @@ class FusedCrossEntropy(torch.autograd.Function):
         elif any(want):
             loss, _, lse, dH, dW = _fused_ce_fwd_bwd(
                 hidden, W, labels, row_weight, reduction=reduction, workspace=None, out=None,
-                grad_dtype=torch.bfloat16, n_valid_total=0, want=want, want_lse=True, **kw)
-            ctx.grads = (dH, dW)
+                grad_dtype=grad_dtype, n_valid_total=0, want=want,
+                want_lse=not ctx.kept, **kw)
             value = loss[0]
+            if ctx.kept:
+                ctx.save_for_backward(dH, dW)
+                return value
+            ctx.grads = (dH, dW)
         else:
             loss, _, lse = fused_ce_fwd(hidden, W, labels, row_weight, reduction=reduction, **kw)
             value = loss[0]
@@ -645,9 +652,12 @@ class FusedCrossEntropy(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out):
-        none = (None,) * 6
+        none = (None,) * 7
         if grad_out is None:
             return (None, None) + none
+        if ctx.kept:        # the product in float32, rounded as it is stored
+            return tuple(t if t is None else torch.mul(t, grad_out, out=torch.empty_like(
+                t, dtype=torch.bfloat16)) for t in ctx.saved_tensors) + none
         hidden, W, labels, row_weight, lse = ctx.saved_tensors
         if ctx.grads is not None:
             (dH, dW), ctx.grads = ctx.grads, None
@@ -671,12 +681,19 @@ class FusedCrossEntropy(torch.autograd.Function):
 
 def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0,
                              z_loss=0.0, ignore_index=-100, reduction="mean", chunk=0, check=True,
-                             norm=None):
+                             norm=None, grad_dtype=torch.bfloat16):
     """Differentiable fused_ce_fwd: the loss (a scalar), or with reduction "none"
-    the row losses [N].  hidden and W are bfloat16; ``row_weight`` gets no
-    gradient.  ``check=False`` leaves out the device-error check, which
-    synchronises the stream.  ``norm``: a TailNorm; ``hidden`` is then the
-    residual stream, and the loss runs over its normed rows."""
+    the row losses [N].  hidden and W are bfloat16, and so are their gradients;
+    ``row_weight`` gets no gradient.  ``check=False`` leaves out the device-error
+    check, which synchronises the stream.  ``norm``: a TailNorm; ``hidden`` is then
+    the residual stream, and the loss runs over its normed rows.
+
+    ``grad_dtype``: what the gradients of a mean or sum are held in until backward
+    brings their upstream factor (alpha in "alpha * loss + ..."): bfloat16, which
+    costs nothing at a factor of 1 and a second rounding at one that is not a power
+    of two, or float32, rounded once (twice the memory, one more pass)."""
+    if grad_dtype not in _GRAD_TYPES:
+        raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
     if row_weight is not None and row_weight.requires_grad:
         raise ValueError("row_weight gets no gradient; detach it")
     if reduction not in ("mean", "sum", "none"):
@@ -688,7 +705,7 @@ def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_sm
     if not torch.is_grad_enabled():  # (inside a Function's forward this cannot be told)
         hidden, W = hidden.detach(), W.detach()
     return FusedCrossEntropy.apply(hidden, W, labels, row_weight, reduction, _int(ignore_index),
-                                   check, opts)
+                                   check, opts, grad_dtype)
 
 
 # ---------------------------------------------------------------- norms around a block

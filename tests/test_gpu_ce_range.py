@@ -14,7 +14,8 @@ import torch
 import oracle
 import synth
 from chunked_kl_loss_tcgen05_b200 import fckl_profile_begin, fckl_profile_end
-from chunked_kl_loss_tcgen05_b200.torch_api import fused_ce_bwd, fused_ce_fwd, fused_ce_fwd_bwd
+from chunked_kl_loss_tcgen05_b200.torch_api import (fused_ce_bwd, fused_ce_fwd, fused_ce_fwd_bwd,
+                                                    fused_cross_entropy_loss)
 
 pytestmark = pytest.mark.gpu
 BF16, FP16 = 2.0 ** -8, 2.0 ** -11
@@ -137,3 +138,31 @@ def test_long_sums_of_one_sign(N):
     off = (dW / (q.t() @ h.double() / N) - 1)[1:]
     assert off.mean().abs().item() <= 49152 / 16 * 2.0 ** -23
     assert off.abs().max().item() <= 49152 / 16 * 2.0 ** -23 + 8 * BF16 / N ** 0.5
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(reduction="sum"), dict(chunk=64)])
+def test_gradients_kept_in_float32_are_rounded_once(kw):
+    """The gradients of 0.3 loss are those of the float32 call, times 0.3 in float32,
+    rounded once; the same again from a retained graph; frozen operands get none."""
+    N, H, V = 200, 128, 900
+    g = torch.Generator(device="cuda").manual_seed(1)
+    h = torch.randn(N, H, generator=g, device="cuda").bfloat16()
+    W = (torch.randn(V, H, generator=g, device="cuda") * 0.1).bfloat16()
+    y = torch.randint(0, V, (N,), generator=g, device="cuda")
+    weight = torch.rand(N, generator=g, device="cuda")
+    kw = dict(kw, row_weight=weight)
+    direct = fused_ce_fwd_bwd(h, W, y, **kw)
+    factor = torch.tensor(0.3, device="cuda")
+    for frozen in (None, 0, 1):
+        leaves = [t.clone().requires_grad_(i != frozen) for i, t in enumerate((h, W))]
+        loss = fused_cross_entropy_loss(*leaves, y, grad_dtype=torch.float32, **kw)
+        assert torch.equal(loss, direct[0][0])
+        wanted = [i for i in (0, 1) if i != frozen]
+        for scale in (factor, factor * 7):
+            got = torch.autograd.grad(loss * scale, [leaves[i] for i in wanted], retain_graph=True)
+            for i, t in zip(wanted, got):
+                assert torch.equal(t, (direct[2 + i] * scale).bfloat16())
+    rows = fused_cross_entropy_loss(leaves[0], leaves[1], y, reduction="none",
+                                    grad_dtype=torch.float32)
+    rows.sum().backward()
+    assert leaves[0].grad.dtype == torch.bfloat16

@@ -108,3 +108,12 @@ def test_whole_number_options_refuse_fractions(calls):
         with pytest.raises(TypeError):
             ta.fused_ce_fwd(h, W, y, check=False, **{name: 1.5})
     assert not calls
+
+
+def test_held_gradients_are_float32_or_bfloat16(calls):
+    h, W, y = _ce_args()
+    with pytest.raises(TypeError, match="grad_dtype"):
+        ta.fused_cross_entropy_loss(h.requires_grad_(), W, y, grad_dtype=torch.float16)
+    for dtype in (torch.float32, torch.bfloat16):
+        ta.fused_cross_entropy_loss(h.requires_grad_(), W, y, grad_dtype=dtype, check=False)
+    assert [p.grad_type for p in calls] == [0, 1]
