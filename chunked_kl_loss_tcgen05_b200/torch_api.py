@@ -622,11 +622,11 @@ class FusedCrossEntropy(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, hidden, W, labels, row_weight, reduction, ignore_index, check, opts,
-                grad_dtype=torch.bfloat16):
+                grad_dtype=torch.bfloat16, n_valid_total=0):
         want = ctx.needs_input_grad[:2]
         ctx.set_materialize_grads(False)
         ctx.reduction, ctx.ignore_index, ctx.check, ctx.opts = reduction, ignore_index, check, opts
-        ctx.want, ctx.grads = want, None
+        ctx.want, ctx.grads, ctx.n_valid_total = want, None, n_valid_total
         kw = dict(ignore_index=ignore_index, check=check, **opts)
         ctx.kept = reduction != "none" and any(want) and grad_dtype == torch.float32
         if reduction == "none":
@@ -636,7 +636,7 @@ class FusedCrossEntropy(torch.autograd.Function):
         elif any(want):
             loss, _, lse, dH, dW = _fused_ce_fwd_bwd(
                 hidden, W, labels, row_weight, reduction=reduction, workspace=None, out=None,
-                grad_dtype=grad_dtype, n_valid_total=0, want=want,
+                grad_dtype=grad_dtype, n_valid_total=n_valid_total, want=want,
                 want_lse=not ctx.kept, **kw)
             value = loss[0]
             if ctx.kept:
@@ -644,7 +644,8 @@ class FusedCrossEntropy(torch.autograd.Function):
                 return value
             ctx.grads = (dH, dW)
         else:
-            loss, _, lse = fused_ce_fwd(hidden, W, labels, row_weight, reduction=reduction, **kw)
+            loss, _, lse = fused_ce_fwd(hidden, W, labels, row_weight, reduction=reduction,
+                                        n_valid_total=n_valid_total, **kw)
             value = loss[0]
         ctx.save_for_backward(hidden, W, labels, row_weight, lse)
         return value
@@ -652,7 +653,7 @@ class FusedCrossEntropy(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out):
-        none = (None,) * 7
+        none = (None,) * 8
         if grad_out is None:
             return (None, None) + none
         if ctx.kept:        # the product in float32, rounded as it is stored
@@ -670,9 +671,11 @@ class FusedCrossEntropy(torch.autograd.Function):
             if row_weight is not None:
                 row_grad = row_grad * row_weight
             if ctx.reduction == "mean":
-                V = W.shape[0]
-                kept = (labels != ctx.ignore_index) & (labels >= 0) & (labels < V)
-                row_grad = row_grad / kept.sum().clamp(min=1)
+                V, count = W.shape[0], ctx.n_valid_total
+                if count == 0:
+                    kept = (labels != ctx.ignore_index) & (labels >= 0) & (labels < V)
+                    count = kept.sum().clamp(min=1)
+                row_grad = row_grad / count
         dH, dW = fused_ce_bwd(hidden, W, labels, lse, row_grad.contiguous(),
                               ignore_index=ctx.ignore_index, check=ctx.check,
                               grad_dtype=torch.bfloat16, want=ctx.want, **ctx.opts)
@@ -681,13 +684,16 @@ class FusedCrossEntropy(torch.autograd.Function):
 
 def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=0.0,
                              z_loss=0.0, ignore_index=-100, reduction="mean", chunk=0, check=True,
-                             norm=None, grad_dtype=torch.bfloat16):
+                             norm=None, grad_dtype=torch.bfloat16, n_valid_total=0):
     """Differentiable fused_ce_fwd: the loss (a scalar), or with reduction "none"
     the row losses [N].  hidden and W are bfloat16, and so are their gradients;
     ``row_weight`` gets no gradient.  ``check=False`` leaves out the device-error
     check, which synchronises the stream.  ``norm``: a TailNorm; ``hidden`` is then
     the residual stream, and the loss runs over its normed rows.
 
+    ``n_valid_total``: > 0 replaces the number of rows that a mean divides by, e.g.
+    that of all data-parallel ranks' rows: the ranks' losses and gradients then sum
+    to those of the whole batch.
     ``grad_dtype``: what the gradients of a mean or sum are held in until backward
     brings their upstream factor (alpha in "alpha * loss + ..."): bfloat16, which
     costs nothing at a factor of 1 and a second rounding at one that is not a power
@@ -705,7 +711,7 @@ def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_sm
     if not torch.is_grad_enabled():  # (inside a Function's forward this cannot be told)
         hidden, W = hidden.detach(), W.detach()
     return FusedCrossEntropy.apply(hidden, W, labels, row_weight, reduction, _int(ignore_index),
-                                   check, opts, grad_dtype)
+                                   check, opts, grad_dtype, _int(n_valid_total))
 
 
 # ---------------------------------------------------------------- norms around a block

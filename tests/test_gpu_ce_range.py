@@ -166,3 +166,38 @@ def test_gradients_kept_in_float32_are_rounded_once(kw):
                                     grad_dtype=torch.float32)
     rows.sum().backward()
     assert leaves[0].grad.dtype == torch.bfloat16
+
+
+@pytest.mark.parametrize("grad_dtype", [torch.bfloat16, torch.float32])
+def test_mean_over_the_rows_of_all_shards(grad_dtype):
+    """Two shards of a batch, each dividing by the kept rows of both: their losses and
+    gradients are those of the direct calls, from a retained graph too, and sum to the
+    whole batch's."""
+    N, H, V, cut = 150, 64, 400, 61
+    g = torch.Generator(device="cuda").manual_seed(2)
+    h = torch.randn(N, H, generator=g, device="cuda").bfloat16()
+    W = (torch.randn(V, H, generator=g, device="cuda") * 0.1).bfloat16()
+    y = torch.randint(0, V, (N,), generator=g, device="cuda")
+    y[::5] = -100
+    total = int((y >= 0).sum())
+    losses, sums = [], torch.zeros(V, H, device="cuda")
+    for rows in (slice(0, cut), slice(cut, N)):
+        leaves = [h[rows].clone().requires_grad_(), W.clone().requires_grad_()]
+        loss = fused_cross_entropy_loss(*leaves, y[rows], n_valid_total=total,
+                                        grad_dtype=grad_dtype)
+        direct = fused_ce_fwd_bwd(h[rows], W, y[rows], n_valid_total=total)
+        for _ in range(2):
+            got = torch.autograd.grad(loss, leaves, retain_graph=True)
+            for t, d in zip(got, direct[2:]):
+                # bf16 of the same sums; computed again, the dlogits may fall on the
+                # other side of a rounding
+                e = (t.float() - d).norm() / d.norm()
+                assert e.item() <= BF16
+        with torch.no_grad():
+            alone = fused_cross_entropy_loss(*leaves, y[rows], n_valid_total=total)
+        assert alone.item() == pytest.approx(loss.item(), rel=1e-6)
+        losses.append(loss.item())
+        sums += direct[3]
+    whole = fused_ce_fwd_bwd(h, W, y)
+    assert sum(losses) == pytest.approx(whole[0].item(), rel=1e-6)
+    assert ((sums - whole[3]).norm() / whole[3].norm()).item() <= 2.0 ** -12

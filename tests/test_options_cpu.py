@@ -117,3 +117,11 @@ def test_held_gradients_are_float32_or_bfloat16(calls):
     for dtype in (torch.float32, torch.bfloat16):
         ta.fused_cross_entropy_loss(h.requires_grad_(), W, y, grad_dtype=dtype, check=False)
     assert [p.grad_type for p in calls] == [0, 1]
+
+
+def test_mean_over_more_rows_than_the_call_s(calls):
+    h, W, y = _ce_args()
+    loss = ta.fused_cross_entropy_loss(h.requires_grad_(), W, y, n_valid_total=40, check=False)
+    with torch.no_grad():
+        ta.fused_cross_entropy_loss(h, W, y, n_valid_total=40, check=False)
+    assert [p.n_valid_total for p in calls] == [40, 40]
