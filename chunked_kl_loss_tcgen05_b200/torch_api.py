@@ -688,8 +688,10 @@ def fused_cross_entropy_loss(hidden, W, labels, row_weight=None, T=1.0, label_sm
     """Differentiable fused_ce_fwd: the loss (a scalar), or with reduction "none"
     the row losses [N].  hidden and W are bfloat16, and so are their gradients;
     ``row_weight`` gets no gradient.  ``check=False`` leaves out the device-error
-    check, which synchronises the stream.  ``norm``: a TailNorm; ``hidden`` is then
-    the residual stream, and the loss runs over its normed rows.
+    check, which synchronises the stream (a step that is captured into a graph needs
+    that, and, like every captured backward pass, no eager graph of the same leaves
+    alive).  ``norm``: a TailNorm; ``hidden`` is then the residual stream, and the loss
+    runs over its normed rows.
 
     ``n_valid_total``: > 0 replaces the number of rows that a mean divides by, e.g.
     that of all data-parallel ranks' rows: the ranks' losses and gradients then sum

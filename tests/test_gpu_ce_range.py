@@ -15,7 +15,7 @@ import oracle
 import synth
 from chunked_kl_loss_tcgen05_b200 import fckl_profile_begin, fckl_profile_end
 from chunked_kl_loss_tcgen05_b200.torch_api import (fused_ce_bwd, fused_ce_fwd, fused_ce_fwd_bwd,
-                                                    fused_cross_entropy_loss)
+                                                    fused_cross_entropy_loss, TailNorm)
 
 pytestmark = pytest.mark.gpu
 BF16, FP16 = 2.0 ** -8, 2.0 ** -11
@@ -201,3 +201,46 @@ def test_mean_over_the_rows_of_all_shards(grad_dtype):
     whole = fused_ce_fwd_bwd(h, W, y)
     assert sum(losses) == pytest.approx(whole[0].item(), rel=1e-6)
     assert ((sums - whole[3]).norm() / whole[3].norm()).item() <= 2.0 ** -12
+
+
+@pytest.mark.parametrize("grad_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+def test_captured_step_through_the_tail(reduction, grad_dtype):
+    """Loss and gradients of a student's tail captured as one graph; replays on new
+    inputs give the eager step's results.  (No eager graph of the leaves lives during the
+    capture: torch's engine would synchronise with the stream it was made on, which
+    invalidates any capture of a backward pass.)"""
+    N, H, V = 300, 128, 700
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def inputs():
+        return (torch.randn(N, H, generator=g, device="cuda").bfloat16(),
+                torch.randint(0, V, (N,), generator=g, device="cuda"))
+
+    x, y = inputs()
+    x.requires_grad_()
+    W = (torch.randn(V, H, generator=g, device="cuda") * 0.1).bfloat16().requires_grad_()
+    w2 = torch.rand(H, generator=g, device="cuda").requires_grad_()
+    leaves, up = (x, W, w2), torch.rand(N, generator=g, device="cuda")
+
+    def step():
+        loss = fused_cross_entropy_loss(x, W, y, reduction=reduction, check=False,
+                                        norm=TailNorm(pre_weight=w2), grad_dtype=grad_dtype)
+        return (loss, *torch.autograd.grad(loss, leaves, up if reduction == "none" else up[0]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(3):
+        nx, ny = inputs()
+        with torch.no_grad():
+            x.copy_(nx), y.copy_(ny), up.mul_(0.7)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, step()))
