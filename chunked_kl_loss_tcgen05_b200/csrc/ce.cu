@@ -39,8 +39,8 @@ constexpr double kCutShare = 0.14;
 
 // Calls of one row tile run their dH GEMM (which reads W) and their dW GEMM (which
 // writes as much) side by side, on 3/8 and 5/8 of the CTA pairs, unless W is large:
-// small ones are bound by launches and tails, large ones by what an SM can store, and
-// there dW needs all of them.  More rows carry it further with bf16 gradients, where
+// small ones are bound by launches and tails, large ones by memory, and with 5/8 of
+// the pairs dW does not reach its rate.  More rows carry it further with bf16 gradients, where
 // the products grow and dW's bytes do not; fp32 ones cost more when dH goes first.
 // Graph-timed steps with L2 flushed, us, one after the other and side by side; bf16
 // gradients: 256 x 256 x 4096 37 and 35, 16 x 512 x 32000 55 and 51, 256 x 1024 x 32000 96
@@ -107,7 +107,8 @@ long long ce_rows(const fckl_ce_problem* p) {
 }
 
 // Scoring calls of one or two rows stream W past them instead of multiplying
-// tiles of 256 rows, whose products alone take 157 us at 4096 x 128256 (bytes: 163).
+// tiles of 256 rows, whose products alone take 157 us at 4096 x 128256 (W's bytes: 163
+// at a copy's rate, which a read alone beats).
 // Graph-timed, us, tiles and streamed: one row 4096 x 128256 184 and 157, 2048 x 32000
 // 38 and 28, 1344 x 583 19 and 10; two rows of 4096 x 128256 184 and 170.  Four rows
 // (184 and 188) and eight (184 and 373) are bound by the sums' arithmetic.

@@ -360,6 +360,9 @@ fckl_status fckl_ce_fwd(const fckl_ce_problem* prob, const void* hidden, const v
 /* Forward and backward in one call: dH [N, H] and dW [V, H] of `loss`, in
  * grad_type, overwritten.  row_loss and lse may be NULL, and so may one of dH
  * and dW (a frozen projection, or frozen rows: that product is not computed).
+ * dlogits are rounded to bf16 ahead of both products, whatever grad_type is: a
+ * gradient is off by about 1e-3 to 2e-3 of itself (norms), fp32 ones too, which only
+ * spare the result's own rounding.
  * 6*H*V flops per kept row: the forward keeps one chunk's exponentials in the
  * block that dlogits then takes (8*H*V for short hidden rows, H <= 384, against
  * large vocabularies, where computing the logits again costs less). */
