@@ -40,8 +40,9 @@ constexpr double kCutShare = 0.14;
 // Calls of one row tile run their dH GEMM (which reads W) and their dW GEMM (which
 // writes as much) side by side, on 3/8 and 5/8 of the CTA pairs, unless W is large:
 // small ones are bound by launches and tails, large ones by memory, and with 5/8 of
-// the pairs dW does not reach its rate.  More rows carry it further with bf16 gradients, where
-// the products grow and dW's bytes do not; fp32 ones cost more when dH goes first.
+// the pairs dW does not reach its rate.  More rows carry it further with bf16
+// gradients, where the products grow and dW's bytes do not; fp32 ones cost more when
+// dH goes first.
 // Graph-timed steps with L2 flushed, us, one after the other and side by side; bf16
 // gradients: 256 x 256 x 4096 37 and 35, 16 x 512 x 32000 55 and 51, 256 x 1024 x 32000 96
 // and 86, 16 x 2880 x 8192 66 and 70, 64 x 1024 x 50257 96 and 107, 128 x 4096 x 128256

@@ -17,10 +17,10 @@
 //
 // Bound by HBM: forward x, b in and v, y out; backward x, b, dy, dv in and dx,
 // db out.  16384 rows of 4096 in bf16, whole calls: 89 to 102 us (82 to 93% of a
-// copy's speed) and 143 to 158 us (79 to 87%).  Rows go through a ring of shared-memory stages filled by 16-byte
-// asynchronous copies, several rows ahead; a thread copies exactly the values
-// it will read, so the data needs no barrier, and the waits are the copies'
-// own.  A long row takes a block, a short one 32, 16 or 8 lanes of a warp (8, 16
+// copy's speed) and 143 to 158 us (79 to 87%).  Rows go through a ring of
+// shared-memory stages filled by 16-byte asynchronous copies, several rows ahead; a
+// thread copies exactly the values it will read, so the data needs no barrier, and
+// the waits are the copies' own.  A long row takes a block, a short one 32, 16 or 8 lanes of a warp (8, 16
 // or 32 rows a block).  What limits the kernels below HBM speed is latency, of
 // shuffles and barriers first: so all sums of a row go through one reduction,
 // which also carries the next row's sum of b^2 (the only one that has to come

@@ -555,7 +555,8 @@ def fused_ce_fwd_bwd(hidden, W, labels, row_weight=None, T=1.0, label_smoothing=
     """fused_ce_fwd with the gradients of ``loss`` in the same call: returns
     (loss[1], row_loss[N], dH[N,H], dW[V,H]), the gradients in ``grad_dtype``
     (float32 or bfloat16; either way the dlogits are rounded to bfloat16 for the
-    tensor cores, so float32 spares the result's own rounding and no more).  ``out``: optional (loss, dH, dW) to write into."""
+    tensor cores, so float32 spares the result's own rounding and no more).
+    ``out``: optional (loss, dH, dW) to write into."""
     loss, row_loss, _, dH, dW = _fused_ce_fwd_bwd(
         hidden, W, labels, row_weight, T, label_smoothing, z_loss, ignore_index, reduction, chunk,
         workspace, check, out, grad_dtype, n_valid_total)
@@ -567,7 +568,8 @@ def fused_ce_bwd(hidden, W, labels, lse, row_grad, T=1.0, label_smoothing=0.0, z
                  grad_dtype=torch.float32, want=(True, True)):
     """Gradients of sum(row_grad * row_loss) for the row losses and ``lse`` that
     fused_ce_fwd returned on the same inputs; row_grad float32 [N], of either
-    sign.  Returns (dH[N,H], dW[V,H]) in ``grad_dtype`` (see fused_ce_fwd_bwd); ``want`` = (dH, dW): leave one out (None)."""
+    sign.  Returns (dH[N,H], dW[V,H]) in ``grad_dtype`` (see fused_ce_fwd_bwd);
+    ``want`` = (dH, dW): leave one out (None)."""
     if lse is None or row_grad is None:
         raise TypeError("lse and row_grad must be float32 tensors [N]")
     if not any(want):

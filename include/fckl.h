@@ -339,7 +339,8 @@ typedef struct {
                             spread evenly over the nearest number of chunks (so
                             3/4 to 3/2 as many, and all N up to 3/2).  dW's
                             partial sums are cut, not rounded, inside a chunk:
-                            up to about rows / 16 * 1e-7 of a sum of one sign */
+                            up to about rows / 16 * 1e-7 of a sum of one sign
+                            (dH's likewise inside a segment of the vocabulary) */
   int64_t n_valid_total; /* mean: > 0 replaces the number of kept rows as D   */
   int32_t label_type;    /* fckl_label_type of labels                         */
   int32_t grad_type;     /* fckl_grad_type of dH and dW                       */
